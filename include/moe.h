@@ -302,6 +302,65 @@ moe_status_t moe_forward_noalloc(const moe_desc_t* desc, const void* x, const vo
                                  const void* W_down, void* out, float* f, float* p,
                                  void* stream);
 
+/* ---- Dense products with a fused epilogue: the projections and dense FFN layers that stand
+ * beside a sparse layer (book 30.2.1: a sparse layer takes the place of one dense FFN; a
+ * shared expert of another width is one too).
+ *   moe_linear        out = act(x W^T + bias) + residual
+ *   moe_linear_gated  out = act(x W_gate^T + bias_gate) * (x W_up^T + bias_up) + residual
+ *   *_fp8             the same with e4m3 codes and one float32 scale per output row, as for
+ *                     the expert weights above (x bf16; the scale multiplies the 32-bit sum,
+ *                     before the bias)
+ *   x [M, K], W [N, K] in desc->dtype (codes: uint8); bias [N] float32 or NULL;
+ *   residual [M, N] in desc->out_dtype or NULL; out [M, N] in desc->out_dtype.
+ * Sums, bias, activation and residual are 32-bit; the one rounding is out's.
+ * The rows of x, W, residual and out may be strided (elements from row to row; 0: packed).
+ * residual may be out itself (same stride); out must not overlap any other argument.
+ * M == 0 enqueues nothing.  Every other convention is that of the entry points above. */
+typedef enum {
+  MOE_ACT_NONE = 0,
+  MOE_ACT_RELU = 1,       /* max(z, 0) */
+  MOE_ACT_GELU = 2,       /* z/2 (1 + erf(z / sqrt 2)) */
+  MOE_ACT_GELU_TANH = 3,  /* z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) */
+  MOE_ACT_SILU = 4        /* z / (1 + exp(-z)) */
+} moe_act_t;
+
+/* Supported: 0 <= M <= 2^24; 1 <= N, K <= 2^20; M N <= 2^40; K and the strides of x and W
+ * multiples of 16 bytes (K: of 16 with 8-bit weights); x and W 16-byte aligned, the other
+ * tensors to their element; strides not below the row's length (else MOE_E_SHAPE) nor above
+ * 2^31. */
+typedef struct {
+  int64_t M, N, K;
+  int64_t ldx, ldw, ldr, ldo;   /* row strides of x, W (both of a gated pair), residual, out */
+  int32_t dtype;                /* moe_dtype_t of x and W */
+  int32_t out_dtype;            /* moe_dtype_t of residual and out */
+  int32_t act;                  /* moe_act_t */
+} moe_linear_desc_t;
+
+/* Host-only check of a description with plain weights (fp8 == 0) or 8-bit ones. */
+moe_status_t moe_linear_validate(const moe_linear_desc_t* desc, int fp8);
+/* Bytes of workspace a call takes (256-byte aligned; gated and fp8 as for the entry point
+ * called); 0: none, NULL may be passed (also for an invalid description).  No HIP call
+ * but the CU count of the current device. */
+size_t moe_linear_workspace_bytes(const moe_linear_desc_t* desc, int gated, int fp8);
+/* Errors: MOE_E_NULL (x, W, scales, out), MOE_E_SHAPE, MOE_E_UNSUPPORTED, MOE_E_WORKSPACE,
+ * MOE_E_HIP. */
+moe_status_t moe_linear(const moe_linear_desc_t* desc, const void* x, const void* W,
+                        const float* bias, const void* residual, void* out, void* workspace,
+                        size_t workspace_bytes, void* stream);
+moe_status_t moe_linear_gated(const moe_linear_desc_t* desc, const void* x, const void* W_gate,
+                              const void* W_up, const float* bias_gate, const float* bias_up,
+                              const void* residual, void* out, void* workspace,
+                              size_t workspace_bytes, void* stream);
+moe_status_t moe_linear_fp8(const moe_linear_desc_t* desc, const void* x, const uint8_t* Wq,
+                            const float* s, const float* bias, const void* residual, void* out,
+                            void* workspace, size_t workspace_bytes, void* stream);
+moe_status_t moe_linear_gated_fp8(const moe_linear_desc_t* desc, const void* x,
+                                  const uint8_t* Wq_gate, const uint8_t* Wq_up,
+                                  const float* s_gate, const float* s_up,
+                                  const float* bias_gate, const float* bias_up,
+                                  const void* residual, void* out, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -10,6 +10,8 @@ kernels.  The functions mirror the C entry points:
     forward_expert_choice(...), route_expert_choice(...), combine_expert_choice(...)
     forward_next_best(...), route_next_best(...), dispatch_next_best(...) (capacity
     overflow handed to the next-best expert)
+    linear(...), linear_gated(...), linear_fp8(...), linear_gated_fp8(...) (dense products
+    with bias, activation and residual in the epilogue)
 
 There is no fallback: without the built library (python -m
 sparse_mixture_experts_24_amd.build) every call raises.
@@ -35,7 +37,9 @@ EXPORTS = ("moe_status_str", "moe_validate", "moe_workspace_bytes", "moe_capacit
            "moe_workspace_bytes_expert_choice", "moe_capacity_expert_choice",
            "moe_route_expert_choice", "moe_combine_expert_choice", "moe_forward_expert_choice",
            "moe_forward_next_best", "moe_route_next_best", "moe_dispatch_next_best",
-           "moe_forward_noalloc")
+           "moe_forward_noalloc", "moe_linear_validate", "moe_linear_workspace_bytes",
+           "moe_linear", "moe_linear_gated", "moe_linear_fp8", "moe_linear_gated_fp8")
+ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 # Bytes of the library's static device scratch that moe_forward_noalloc uses (moe.h).
 NOALLOC_SCRATCH_BYTES = 64 << 20
 
@@ -46,6 +50,15 @@ class MoeDesc(ctypes.Structure):
         ("d_ff", ctypes.c_int64), ("top_k", ctypes.c_int64), ("n_shared", ctypes.c_int64),
         ("capacity_factor", ctypes.c_float), ("dtype", ctypes.c_int32),
         ("out_dtype", ctypes.c_int32),
+    ]
+
+
+class LinearDesc(ctypes.Structure):
+    _fields_ = [
+        ("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
+        ("ldx", ctypes.c_int64), ("ldw", ctypes.c_int64), ("ldr", ctypes.c_int64),
+        ("ldo", ctypes.c_int64), ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+        ("act", ctypes.c_int32),
     ]
 
 
@@ -117,6 +130,19 @@ def lib():
         L.moe_dispatch_next_best.argtypes = [D, P, P, P, P, P, P, P, S, P]
         L.moe_forward_noalloc.restype = I
         L.moe_forward_noalloc.argtypes = [D, P, P, P, P, P, P, P, P, P, P]
+        LD = ctypes.POINTER(LinearDesc)
+        L.moe_linear_validate.restype = I
+        L.moe_linear_validate.argtypes = [LD, I]
+        L.moe_linear_workspace_bytes.restype = S
+        L.moe_linear_workspace_bytes.argtypes = [LD, I, I]
+        L.moe_linear.restype = I
+        L.moe_linear.argtypes = [LD, P, P, P, P, P, P, S, P]
+        L.moe_linear_gated.restype = I
+        L.moe_linear_gated.argtypes = [LD, P, P, P, P, P, P, P, P, S, P]
+        L.moe_linear_fp8.restype = I
+        L.moe_linear_fp8.argtypes = [LD, P, P, P, P, P, P, P, S, P]
+        L.moe_linear_gated_fp8.restype = I
+        L.moe_linear_gated_fp8.argtypes = [LD, P, P, P, P, P, P, P, P, P, P, S, P]
         _lib = L
     return _lib
 
@@ -619,3 +645,109 @@ def dispatch_next_best(topk_idx, cand, n_experts, capacity_factor, workspace=Non
                                       _stream(dev))
     _check("moe_dispatch_next_best", st)
     return counts, offsets, perm, slot
+
+
+# ----------------------------------------------------------------------------- dense products
+def _rows(t, name, device, dtype, shape):
+    """Checks a [rows, cols] tensor whose rows may be strided; returns its row stride."""
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    ld = t.stride(0) if shape[0] > 1 else shape[1]
+    if ld < shape[1]:
+        raise ValueError(f"{name} has overlapping rows (row stride {ld})")
+    return ld
+
+
+def _opt_ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def linear_desc(x, W, act="none", residual=None, out=None, out_dtype=None, fp8=False):
+    """Description of a dense product of x [M, K] and W [N, K] (strides as the tensors')."""
+    dev = x.device
+    if x.dim() != 2 or W.dim() != 2:
+        raise ValueError("x and W must be matrices")
+    if act not in ACTS:
+        raise ValueError(f"act {act!r} is none of {', '.join(ACTS)}")
+    M, K = x.shape
+    N = W.shape[0]
+    odt = out_dtype or x.dtype
+    ldx = _rows(x, "x", dev, x.dtype, (M, K))
+    ldw = _rows(W, "W", dev, torch.uint8 if fp8 else x.dtype, (N, K))
+    ldr = 0 if residual is None else _rows(residual, "residual", dev, odt, (M, N))
+    ldo = 0 if out is None else _rows(out, "out", dev, odt, (M, N))
+    return LinearDesc(M, N, K, ldx, ldw, ldr, ldo, _dt(x.dtype), _dt(odt), ACTS[act])
+
+
+def linear_workspace_bytes(desc: LinearDesc, gated=False, fp8=False) -> int:
+    """Bytes of workspace such a call takes (0: none)."""
+    return int(lib().moe_linear_workspace_bytes(ctypes.byref(desc), int(gated), int(fp8)))
+
+
+def _linear(name, x, W, W2, s, s2, b, b2, act, residual, out, out_dtype, workspace):
+    gated, fp8 = W2 is not None, s is not None
+    desc = linear_desc(x, W, act, residual, out, out_dtype, fp8)
+    dev, N = x.device, desc.N
+    if gated and _rows(W2, "W_up", dev, W.dtype, W.shape) != desc.ldw:
+        raise ValueError("W_gate and W_up must have the same row stride")
+    for t, n in ((b, "bias"), (b2, "bias_up"), (s, "s"), (s2, "s_up")):
+        if t is not None:
+            _require(t, n, dev, torch.float32, (N,))
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _linear(name, x, W, W2, s, s2, b, b2, act, residual, out, out_dtype, workspace)
+    if out is None:
+        out = torch.empty(x.shape[0], N, dtype=out_dtype or x.dtype, device=dev)
+    if workspace is None:
+        n = linear_workspace_bytes(desc, gated, fp8)
+        workspace = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+    args = [x.data_ptr(), W.data_ptr()]
+    if gated:
+        args.append(W2.data_ptr())
+    if fp8:
+        args.append(s.data_ptr())
+        if gated:
+            args.append(s2.data_ptr())
+    args.append(_opt_ptr(b))
+    if gated:
+        args.append(_opt_ptr(b2))
+    args += [_opt_ptr(residual), out.data_ptr(), _opt_ptr(workspace),
+             0 if workspace is None else workspace.numel(),
+             torch.cuda.current_stream(dev).cuda_stream]
+    _check(name, getattr(lib(), name)(ctypes.byref(desc), *args))
+    return out
+
+
+def linear(x, W, bias=None, act="none", residual=None, out=None, out_dtype=None, workspace=None):
+    """act(x W^T + bias) + residual: x [M, K], W [N, K] (rows of either, of residual and of
+    out may be strided), bias [N] float32, residual and out [M, N] in out_dtype.  residual may
+    be out itself.  Returns out."""
+    return _linear("moe_linear", x, W, None, None, None, bias, None, act, residual, out,
+                   out_dtype, workspace)
+
+
+def linear_gated(x, W_gate, W_up, bias_gate=None, bias_up=None, act="silu", residual=None,
+                 out=None, out_dtype=None, workspace=None):
+    """act(x W_gate^T + bias_gate) * (x W_up^T + bias_up) + residual; arguments as linear."""
+    return _linear("moe_linear_gated", x, W_gate, W_up, None, None, bias_gate, bias_up, act,
+                   residual, out, out_dtype, workspace)
+
+
+def linear_fp8(x, Wq, s, bias=None, act="none", residual=None, out=None, out_dtype=None,
+               workspace=None):
+    """linear with W = s * decode(Wq): e4m3 codes [N, K] uint8, one float32 scale per row."""
+    return _linear("moe_linear_fp8", x, Wq, None, s, None, bias, None, act, residual, out,
+                   out_dtype, workspace)
+
+
+def linear_gated_fp8(x, Wq_gate, Wq_up, s_gate, s_up, bias_gate=None, bias_up=None, act="silu",
+                     residual=None, out=None, out_dtype=None, workspace=None):
+    """linear_gated with 8-bit weights, as linear_fp8."""
+    return _linear("moe_linear_gated_fp8", x, Wq_gate, Wq_up, s_gate, s_up, bias_gate, bias_up,
+                   act, residual, out, out_dtype, workspace)

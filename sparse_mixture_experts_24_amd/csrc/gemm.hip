@@ -1321,7 +1321,7 @@ hipError_t launch_zero_i32(int32_t* p, int n, hipStream_t s) {
 // Facts about the current device, looked up once per device (the library may drive
 // several GPUs from several threads).
 
-static int device_cu_count() {
+int device_cu_count() {
   static std::atomic<int> cached[kMaxDevices];   // 0: not looked up yet
   int dev = 0;
   if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kMaxDevices) return 256;

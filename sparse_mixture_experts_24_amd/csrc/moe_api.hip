@@ -11,7 +11,7 @@
 
 namespace moe {
 
-static moe_status_t validate(const moe_desc_t* d) {
+moe_status_t validate(const moe_desc_t* d) {
   if (!d) return MOE_E_NULL;
   if (d->T < 0 || d->d_model <= 0 || d->n_experts < 1 || d->d_ff <= 0 || d->top_k < 1 ||
       d->top_k > d->n_experts || d->n_shared < 0 || d->n_shared > 1 ||
@@ -82,7 +82,7 @@ static moe_status_t check_ws(const moe_desc_t& d, void* ws, size_t bytes, Worksp
 // integer arithmetic (m k T < 2^54 under validate()'s bounds) and no evaluation order or
 // rounding enters.  A C above T k keeps every assignment (an expert holds at most one
 // slot per token), so it is reported as T k, which also keeps C within 32 bits.
-static int64_t capacity_of(const moe_desc_t& d) {
+int64_t capacity_of(const moe_desc_t& d) {
   if (!(d.capacity_factor > 0.0f)) return -1;
   const int64_t all = d.T * d.top_k;
   int e2 = 0;

@@ -29,6 +29,14 @@ __device__ inline bf16_t f32_to_bf16(float f) {
   return (bf16_t)(u >> 16);
 }
 
+// ---------------------------------------------------------------- host checks
+// MOE_OK or the status every entry point returns for this description.
+moe_status_t validate(const moe_desc_t* d);
+// Per-expert capacity max(floor(cf k T / E), k) of a valid description, -1 without one.
+int64_t capacity_of(const moe_desc_t& d);
+// Compute units of the current device (looked up once per device).
+int device_cu_count();
+
 // ---------------------------------------------------------------- route plan
 // One route block handles BT = 16 * TPW tokens with 4 waves: EW waves split the
 // (padded) experts into slabs of 16 * EPW, KS = 4 / EW waves split the reduction.
