@@ -361,6 +361,31 @@ moe_status_t moe_linear_gated_fp8(const moe_linear_desc_t* desc, const void* x,
                                   const void* residual, void* out, void* workspace,
                                   size_t workspace_bytes, void* stream);
 
+/* ---- The layer for a few tokens: at most MOE_FEW_TOKENS of them, as in single-token or
+ * small-batch decoding, where moe_forward is bound by its launches and by one workgroup's
+ * routing as much as by the weights.
+ *   moe_forward_few      moe_forward, with residual [T, d] (desc->out_dtype, or NULL) added:
+ *                        out = layer(x) + residual
+ *   moe_forward_few_fp8  the same with 8-bit expert weights (moe_forward_fp8)
+ * Same layer, layouts and rules as moe_forward (capacity and shared expert included); h is
+ * carried with the precision of float32 sums, not rounded to bf16, so outputs are at least
+ * as exact as moe_forward's and may differ from them by that rounding.  Without a capacity
+ * a token's output does not depend on the other tokens of the call.  residual may be out.
+ * T > MOE_FEW_TOKENS is MOE_E_UNSUPPORTED.  The workspace (256-byte aligned, contents
+ * arbitrary) comes from moe_workspace_bytes_few (0 for an invalid description). */
+#define MOE_FEW_TOKENS 16
+size_t moe_workspace_bytes_few(const moe_desc_t* desc);
+moe_status_t moe_forward_few(const moe_desc_t* desc, const void* x, const void* W_router,
+                             const float* router_bias, const void* W_gate, const void* W_up,
+                             const void* W_down, const void* residual, void* out, float* f,
+                             float* p, void* workspace, size_t workspace_bytes, void* stream);
+moe_status_t moe_forward_few_fp8(const moe_desc_t* desc, const void* x, const void* W_router,
+                                 const float* router_bias, const uint8_t* Wq_gate,
+                                 const uint8_t* Wq_up, const uint8_t* Wq_down,
+                                 const float* s_gate, const float* s_up, const float* s_down,
+                                 const void* residual, void* out, float* f, float* p,
+                                 void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -10,6 +10,7 @@ kernels.  The functions mirror the C entry points:
     forward_expert_choice(...), route_expert_choice(...), combine_expert_choice(...)
     forward_next_best(...), route_next_best(...), dispatch_next_best(...) (capacity
     overflow handed to the next-best expert)
+    forward_few(...), forward_few_fp8(...) (the layer for at most FEW_TOKENS tokens)
     linear(...), linear_gated(...), linear_fp8(...), linear_gated_fp8(...) (dense products
     with bias, activation and residual in the epilogue)
 
@@ -38,7 +39,10 @@ EXPORTS = ("moe_status_str", "moe_validate", "moe_workspace_bytes", "moe_capacit
            "moe_route_expert_choice", "moe_combine_expert_choice", "moe_forward_expert_choice",
            "moe_forward_next_best", "moe_route_next_best", "moe_dispatch_next_best",
            "moe_forward_noalloc", "moe_linear_validate", "moe_linear_workspace_bytes",
-           "moe_linear", "moe_linear_gated", "moe_linear_fp8", "moe_linear_gated_fp8")
+           "moe_linear", "moe_linear_gated", "moe_linear_fp8", "moe_linear_gated_fp8",
+           "moe_workspace_bytes_few", "moe_forward_few", "moe_forward_few_fp8")
+# Most tokens of a forward_few call (moe.h).
+FEW_TOKENS = 16
 ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 # Bytes of the library's static device scratch that moe_forward_noalloc uses (moe.h).
 NOALLOC_SCRATCH_BYTES = 64 << 20
@@ -143,6 +147,12 @@ def lib():
         L.moe_linear_fp8.argtypes = [LD, P, P, P, P, P, P, P, S, P]
         L.moe_linear_gated_fp8.restype = I
         L.moe_linear_gated_fp8.argtypes = [LD, P, P, P, P, P, P, P, P, P, P, S, P]
+        L.moe_workspace_bytes_few.restype = S
+        L.moe_workspace_bytes_few.argtypes = [D]
+        L.moe_forward_few.restype = I
+        L.moe_forward_few.argtypes = [D, P, P, P, P, P, P, P, P, P, P, P, S, P]
+        L.moe_forward_few_fp8.restype = I
+        L.moe_forward_few_fp8.argtypes = [D, P, P, P, P, P, P, P, P, P, P, P, P, P, P, S, P]
         _lib = L
     return _lib
 
@@ -645,6 +655,78 @@ def dispatch_next_best(topk_idx, cand, n_experts, capacity_factor, workspace=Non
                                       _stream(dev))
     _check("moe_dispatch_next_best", st)
     return counts, offsets, perm, slot
+
+
+# ----------------------------------------------------------------------------- few tokens
+def workspace_bytes_few(desc: MoeDesc) -> int:
+    """Bytes of workspace of a forward_few call (0: invalid description)."""
+    return int(lib().moe_workspace_bytes_few(ctypes.byref(desc)))
+
+
+def alloc_workspace_few(desc: MoeDesc, device) -> torch.Tensor:
+    n = workspace_bytes_few(desc)
+    if n == 0:
+        _check("moe_workspace_bytes_few", validate(desc) or 3)
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def _few(name, x, W_router, bias, weights, scales, k, capacity_factor, residual, out, f, p,
+         out_dtype, workspace, want_stats):
+    dev = x.device
+    T, d = x.shape
+    E = W_router.shape[0]
+    G, F, _ = weights[0].shape
+    odt = out_dtype or x.dtype
+    wdt = x.dtype if scales is None else torch.uint8
+    desc = make_desc(T, d, E, F, k, G - E, capacity_factor, x.dtype, odt)
+    _require(x, "x", dev)
+    _require(W_router, "W_router", dev, x.dtype, (E, d))
+    _require(bias, "router_bias", dev, torch.float32, (E,))
+    for w, n, shape in zip(weights, ("W_gate", "W_up", "W_down"),
+                           ((G, F, d), (G, F, d), (G, d, F))):
+        _require(w, n, dev, wdt, shape)
+    for s, n, shape in zip(scales or (), ("s_gate", "s_up", "s_down"), ((G, F), (G, F), (G, d))):
+        _require(s, n, dev, torch.float32, shape)
+    _require(residual, "residual", dev, odt, (T, d))
+    _require(out, "out", dev, odt, (T, d))
+    _require(f, "f", dev, torch.float32, (E,))
+    _require(p, "p", dev, torch.float32, (E,))
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _few(name, x, W_router, bias, weights, scales, k, capacity_factor, residual,
+                        out, f, p, out_dtype, workspace, want_stats)
+    if out is None:
+        out = torch.empty(T, d, dtype=odt, device=dev)
+    if want_stats and f is None:
+        f = torch.empty(E, dtype=torch.float32, device=dev)
+    if want_stats and p is None:
+        p = torch.empty(E, dtype=torch.float32, device=dev)
+    if workspace is None:
+        workspace = alloc_workspace_few(desc, dev)
+    args = [x.data_ptr(), W_router.data_ptr(), _opt_ptr(bias), *[w.data_ptr() for w in weights],
+            *[s.data_ptr() for s in scales or ()], _opt_ptr(residual), out.data_ptr(),
+            _opt_ptr(f), _opt_ptr(p), workspace.data_ptr(), workspace.numel(),
+            torch.cuda.current_stream(dev).cuda_stream]
+    _check(name, getattr(lib(), name)(ctypes.byref(desc), *args))
+    return out, f, p
+
+
+def forward_few(x, W_router, router_bias, W_gate, W_up, W_down, k, capacity_factor=0.0,
+                residual=None, out=None, f=None, p=None, out_dtype=None, workspace=None,
+                want_stats=True):
+    """The whole layer for at most FEW_TOKENS tokens, residual [T, d] (out_dtype) added; it may
+    be out itself.  Arguments otherwise as forward.  Returns (y, f, p)."""
+    return _few("moe_forward_few", x, W_router, router_bias, (W_gate, W_up, W_down), None, k,
+                capacity_factor, residual, out, f, p, out_dtype, workspace, want_stats)
+
+
+def forward_few_fp8(x, W_router, router_bias, Wq_gate, Wq_up, Wq_down, s_gate, s_up, s_down, k,
+                    capacity_factor=0.0, residual=None, out=None, f=None, p=None, out_dtype=None,
+                    workspace=None, want_stats=True):
+    """forward_few with 8-bit expert weights (arguments as forward_fp8)."""
+    return _few("moe_forward_few_fp8", x, W_router, router_bias, (Wq_gate, Wq_up, Wq_down),
+                (s_gate, s_up, s_down), k, capacity_factor, residual, out, f, p, out_dtype,
+                workspace, want_stats)
 
 
 # ----------------------------------------------------------------------------- dense products

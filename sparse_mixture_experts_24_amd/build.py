@@ -18,7 +18,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmoe.so")
 SOURCES = ["moe_api.hip", "route.hip", "dispatch.hip", "gemm.hip", "combine.hip",
-           "expert_choice.hip", "linear.hip"]
+           "expert_choice.hip", "linear.hip", "few.hip"]
 ARCH = "gfx950"
 
 
