@@ -8,13 +8,18 @@
 // the stable rank of an assignment is the number of lower tokens in the set.
 #include <math.h>
 
+#include <type_traits>
+
 #include "moe_internal.h"
+#include "stream.h"
 #include "wave.h"
 
 namespace moe {
 
 constexpr int kFew = MOE_FEW_TOKENS;
-constexpr int kFewThreads = 512, kFewWaves = kFewThreads / 64;
+constexpr int kFewThreads = kStreamThreads, kFewWaves = kStreamWaves;
+
+struct FewRoute;
 
 struct FewArgs {
   const void* x;
@@ -25,9 +30,13 @@ struct FewArgs {
   void* out;
   float* f;
   float* p;
-  float* logits;   // [T, E]
-  float* H;        // [T*k + S*T, F], expert-contiguous rows
+  float* logits;     // [T, E]
+  FewRoute* route;   // the routing, for the kernels after the first expert kernel
+  void* H;           // [T*k + S*T, F] expert-contiguous rows: float, or bf16 values
+  bf16_t* Hlo;       //   and (bf16 layers) the bf16 remainders
+  float* part;       // [T*k + S*T, chunks, d] partial down products
   int T, d, E, F, k, S, C;   // C: capacity, -1 none
+  int chunks;        // parts that the down products' F range is summed in
 };
 
 // The routing of the call, held by every workgroup.
@@ -37,8 +46,9 @@ struct FewRoute {
   int row0[kFew * kMaxTopK + 2];       // first H row of each
   uint16_t mask[kFew * kMaxTopK + 1];  // its kept tokens
   float w[kFew][kMaxTopK];             // renormalised weight of slot j
-  int16_t row[kFew][kMaxTopK + 1];     // H row of slot j, -1 dropped; [k]: the shared row
+  int16_t row[kFew][kMaxTopK + 2];     // H row of slot j, -1 dropped; [k]: the shared row
 };
+static_assert(sizeof(FewRoute) % 4 == 0, "copied as int32");
 
 __device__ inline float wide(const float* p) { return *p; }
 __device__ inline float wide(const bf16_t* p) { return bf16_to_f32(*p); }
@@ -175,85 +185,309 @@ __device__ inline void few_route(const FewArgs& a, FewRoute& r) {
   __syncthreads();
 }
 
+// Router logits of 16 experts per workgroup.
 template <typename XT>
-__global__ __launch_bounds__(256) void few_logits_kernel(FewArgs a) {
-  const int lane = threadIdx.x & 63, i = blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (i >= a.T * a.E) return;
-  const XT* x = (const XT*)a.x + (int64_t)(i / a.E) * a.d;
-  const XT* w = (const XT*)a.Wr + (int64_t)(i % a.E) * a.d;
-  float s = 0.0f;
-  for (int c = lane; c < a.d; c += 64) s = fmaf(wide(x + c), wide(w + c), s);
-  s = wave_sum(s);
-  if (lane == 0) a.logits[i] = s;
+__global__ __launch_bounds__(kFewThreads) void few_logits_kernel(FewArgs a) {
+  __shared__ __align__(16) char stage[kFewWaves][kStageBytes];
+  __shared__ float red[kFewWaves * kRedWave];
+  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+  const int e0 = blockIdx.x * 16, t = lane & 15;
+  const XT* x = (const XT*)a.x + (int64_t)min(t, a.T - 1) * a.d;
+  const char* row[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    row[i] = (const char*)a.Wr +
+             (int64_t)min(e0 + 8 * i + (lane >> 3), a.E - 1) * a.d * (int)sizeof(XT);
+  floatx4 acc = {0.f, 0.f, 0.f, 0.f};
+  stream_rows<XT, 8>(acc, stage[wv], a.d, [&](int i, int byte) { return row[i] + byte; },
+                     [&](int k) { return t < a.T ? x + k : nullptr; });
+  red_put(red + wv * kRedWave, acc);
+  __syncthreads();
+  const int m = tid >> 4, n = tid & 15;
+  if (m < a.T && e0 + n < a.E) a.logits[m * a.E + e0 + n] = red_get(red, kRedWave, m, n);
 }
 
-template <typename XT, typename WT>
+// A workgroup's run of consecutive units of n, as even as they go.
+__device__ inline void share_of(int64_t n, int64_t& i0, int64_t& i1) {
+  i0 = n * blockIdx.x / gridDim.x;
+  i1 = n * (blockIdx.x + 1) / gridDim.x;
+}
+
+// Units of NG x 16 weight rows; NS steps of every row per wave and visit.  A ring of R steps
+// (R divides NS) runs across the visits: as step s is used, step s + R goes out, of this
+// visit or of the next, so a wave always has R NG 2 KB in flight.
+template <typename WT, int R, int NG>
+struct Ring {
+  u32x4 w[R][NG][2];
+  // base[g][i]: the lane's row of load i of group g; st0: first step, nst: steps of the row
+  __device__ __forceinline__ void load(int s, const char* const (&base)[NG][2], int st0, int nst,
+                                       int row_bytes) {
+    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+    const int st = min(st0 + s * kFewWaves + wv, nst - 1);
+    const int byte = min(st * kStepBytes + 16 * (lane & 7), row_bytes - 16);
+#pragma unroll
+    for (int g = 0; g < NG; ++g)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        w[s % R][g][i] = *reinterpret_cast<const u32x4*>(base[g][i] + byte);
+  }
+};
+
+// h = SiLU(x W_gate^T) * (x W_up^T).  A unit is NG x (8 gate rows and the 8 matching up
+// rows) of a touched expert; all T tokens run through it (the matrix cores have the room),
+// and the rows of the tokens that chose the expert are kept.  The token operand of the
+// wave's part of d stays in registers over all units when d fits NS steps per wave.
+template <typename WT, int NS, int R, int NG>
 __global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(FewArgs a) {
+  typedef Stream<WT> S;
+  typedef typename S::X XT;
   __shared__ FewRoute r;
+  __shared__ __align__(16) char stage[kFewWaves][kStageBytes];
+  __shared__ float red[2][kFewWaves * NG * kRedWave];
   few_route(a, r);
-  const int lane = threadIdx.x & 63;
-  const int64_t n = (int64_t)r.nu * a.F, step = (int64_t)gridDim.x * kFewWaves;
-  for (int64_t i = blockIdx.x * kFewWaves + (threadIdx.x >> 6); i < n; i += step) {
-    const int u = (int)(i / a.F);
-    const int64_t wr = (int64_t)r.expert[u] * a.F + i % a.F;
-    const WT* g = (const WT*)a.w.gate + wr * a.d;
-    const WT* up = (const WT*)a.w.up + wr * a.d;
-    int row = r.row0[u];
-    for (uint32_t m = r.mask[u]; m; m &= m - 1, ++row) {
-      const XT* x = (const XT*)a.x + (int64_t)(__ffs(m) - 1) * a.d;
-      float sg = 0.0f, su = 0.0f;
-      for (int c = lane; c < a.d; c += 64) {
-        sg = fmaf(wide(x + c), wide(g + c), sg);
-        su = fmaf(wide(x + c), wide(up + c), su);
+  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+  if (blockIdx.x == 0)
+    for (int i = tid; i < (int)(sizeof(FewRoute) / 4); i += kFewThreads)
+      ((int*)a.route)[i] = ((const int*)&r)[i];
+  const int upe = a.F / (8 * NG);   // units per expert
+  int64_t i0, i1;
+  share_of((int64_t)r.nu * upe, i0, i1);
+  if (i0 == i1) return;
+  const int nst = (a.d + S::SK - 1) / S::SK, row_bytes = a.d * (int)sizeof(WT);
+  const int nchunk = (nst + NS * kFewWaves - 1) / (NS * kFewWaves);
+  const int t = lane & 15, g4 = lane >> 4;
+  u32x4 xs[NS][S::XR];
+  auto load_x = [&](int c) {
+#pragma unroll
+    for (int s = 0; s < NS; ++s)
+#pragma unroll
+      for (int i = 0; i < S::XR; ++i) {
+        const int k = ((c * NS + s) * kFewWaves + wv) * S::SK + S::k_of(g4, i);
+        xs[s][i] = u32x4{0, 0, 0, 0};
+        if (t < a.T && k < a.d)
+          xs[s][i] = *reinterpret_cast<const u32x4*>((const XT*)a.x + (int64_t)t * a.d + k);
       }
-      sg = wave_sum(sg);
-      su = wave_sum(su);
-      if (a.w.fp8) {
-        sg *= a.w.s_gate[wr];
-        su *= a.w.s_up[wr];
-      }
-      if (lane == 0) a.H[(int64_t)row * a.F + i % a.F] = sg / (1.0f + expf(-sg)) * su;
+  };
+  Ring<WT, R, NG> ring;
+  const char* base[NG][2];
+  auto point = [&](int64_t i) {
+    const int u = (int)(i / upe);
+    const int64_t f0 = (int64_t)r.expert[u] * a.F + (i % upe) * (8 * NG) + (lane >> 3);
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      base[g][0] = (const char*)a.w.gate + (f0 + 8 * g) * row_bytes;
+      base[g][1] = (const char*)a.w.up + (f0 + 8 * g) * row_bytes;
     }
+  };
+  floatx4 acc[NG];
+  // chunk c of a unit; in, cn: the next visit, if there is one
+  auto visit = [&](auto more, int c, int64_t in, int cn) {
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        u32x4 w0, w1;
+        stage_in(stage[wv], lane, ring.w[s % R][g][0], ring.w[s % R][g][1]);
+        stage_out(stage[wv], lane, w0, w1);
+        S::mma(acc[g], xs[s], w0, w1);
+      }
+      if (s + R < NS) {
+        ring.load(s + R, base, c * NS * kFewWaves, nst, row_bytes);
+      } else if constexpr (decltype(more)::value) {
+        if (s + R == NS) point(in);
+        ring.load(s + R - NS, base, cn * NS * kFewWaves, nst, row_bytes);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  point(i0);
+#pragma unroll
+  for (int s = 0; s < R; ++s) ring.load(s, base, 0, nst, row_bytes);
+  load_x(0);
+  int par = 0;
+  for (int64_t i = i0; i < i1; ++i) {
+#pragma unroll
+    for (int g = 0; g < NG; ++g) acc[g] = floatx4{0.f, 0.f, 0.f, 0.f};
+    for (int c = 0; c < nchunk; ++c) {
+      if (nchunk > 1) load_x(c);
+      const bool last = c + 1 == nchunk;
+      if (last && i + 1 == i1)
+        visit(std::false_type{}, c, 0, 0);
+      else
+        visit(std::true_type{}, c, last ? i + 1 : i, last ? 0 : c + 1);
+    }
+#pragma unroll
+    for (int g = 0; g < NG; ++g) red_put(red[par] + (wv * NG + g) * kRedWave, acc[g]);
+    __syncthreads();
+    // one half of the workgroup (NG 1: the halves take turns; NG 2: one group each) sums up;
+    // the other buffer is free until it has passed the next barrier
+    const int half = tid >> 8, g = NG == 1 ? 0 : half;
+    if (NG == 2 || half == par) {
+      const int m = (tid >> 4) & 15, n = tid & 15;
+      const int u = (int)(i / upe), f = (int)(i % upe) * (8 * NG) + 8 * g + (n & 7);
+      float v = red_get(red[par] + g * kRedWave, NG * kRedWave, m, n);
+      if (sizeof(WT) == 1)
+        v *= (n < 8 ? a.w.s_gate : a.w.s_up)[(int64_t)r.expert[u] * a.F + f];
+      const float up = __shfl_xor(v, 8, 64);
+      const uint32_t mask = r.mask[u];
+      if (n < 8 && ((mask >> m) & 1u)) {
+        const float h = v / (1.0f + expf(-v)) * up;
+        const int64_t o = (int64_t)(r.row0[u] + __popc(mask & ((1u << m) - 1))) * a.F + f;
+        if constexpr (sizeof(XT) == 4) {
+          ((float*)a.H)[o] = h;
+        } else {
+          const bf16_t hi = f32_to_bf16(h);
+          ((bf16_t*)a.H)[o] = hi;
+          a.Hlo[o] = f32_to_bf16(h - bf16_to_f32(hi));
+        }
+      }
+    }
+    par ^= 1;
   }
 }
 
-template <typename WT, typename OT>
+// Partial down products: a unit is NG x 16 rows of W_down of an expert over one chunk of F
+// (NS steps per wave); the token operand (the expert's rows of h, in bf16 layers value and
+// remainder) stays in registers over the units of an (expert, chunk).
+template <typename WT, int NS, int NG>
 __global__ __launch_bounds__(kFewThreads) void few_down_kernel(FewArgs a) {
+  typedef Stream<WT> S;
+  typedef typename S::X XT;
+  constexpr int NH = sizeof(XT) == 4 ? 1 : 2;   // value, remainder
   __shared__ FewRoute r;
-  FewArgs b = a;
-  b.f = b.p = nullptr;
-  few_route(b, r);
-  const int lane = threadIdx.x & 63;
-  const int64_t n = (int64_t)a.T * a.d, step = (int64_t)gridDim.x * kFewWaves;
-  for (int64_t i = blockIdx.x * kFewWaves + (threadIdx.x >> 6); i < n; i += step) {
-    const int t = (int)(i / a.d), c0 = (int)(i % a.d);
-    float y = 0.0f;
-    for (int j = 0; j < a.k + a.S; ++j) {
-      const int row = r.row[t][j];
-      if (row < 0) continue;
-      int u = 0;
-      while (r.row0[u + 1] <= row) ++u;
-      const int64_t wr = (int64_t)r.expert[u] * a.d + c0;
-      const WT* w = (const WT*)a.w.down + wr * a.F;
-      float s = 0.0f;
-      for (int c = lane; c < a.F; c += 64) s = fmaf(a.H[(int64_t)row * a.F + c], wide(w + c), s);
-      s = wave_sum(s);
-      if (a.w.fp8) s *= a.w.s_down[wr];
-      y += j < a.k ? r.w[t][j] * s : s;
+  __shared__ __align__(16) char stage[kFewWaves][kStageBytes];
+  __shared__ float red[2][kFewWaves * NG * kRedWave];
+  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+  for (int i = tid; i < (int)(sizeof(FewRoute) / 4); i += kFewThreads)
+    ((int*)&r)[i] = ((const int*)a.route)[i];
+  __syncthreads();
+  const int upc = a.d / (16 * NG);   // units per (expert, chunk)
+  int64_t i0, i1;
+  share_of((int64_t)r.nu * a.chunks * upc, i0, i1);
+  if (i0 == i1) return;
+  const int nst = (a.F + S::SK - 1) / S::SK, row_bytes = a.F * (int)sizeof(WT);
+  const int t = lane & 15, g4 = lane >> 4;
+  u32x4 xs[NH][NS][S::XR];
+  Ring<WT, NS, NG> ring;   // a whole visit in flight
+  const char* base[NG][2];
+  auto load_h = [&](int64_t uc) {
+    const int u = (int)(uc / a.chunks), c = (int)(uc % a.chunks);
+    const uint32_t mask = r.mask[u];
+    const bool mine = (mask >> t) & 1u;
+    const int64_t o = (int64_t)(r.row0[u] + __popc(mask & ((1u << t) - 1))) * a.F;
+#pragma unroll
+    for (int s = 0; s < NS; ++s)
+#pragma unroll
+      for (int i = 0; i < S::XR; ++i) {
+        const int k = ((c * NS + s) * kFewWaves + wv) * S::SK + S::k_of(g4, i);
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+          xs[h][s][i] = u32x4{0, 0, 0, 0};
+          if (mine && k < a.F)
+            xs[h][s][i] = *reinterpret_cast<const u32x4*>(
+                (h == 0 ? (const XT*)a.H : (const XT*)a.Hlo) + o + k);
+        }
+      }
+  };
+  int st0 = 0;
+  auto point = [&](int64_t i) {
+    const int64_t uc = i / upc;
+    st0 = (int)(uc % a.chunks) * NS * kFewWaves;
+    const int64_t n0 = (int64_t)r.expert[uc / a.chunks] * a.d + (i % upc) * (16 * NG) + (lane >> 3);
+#pragma unroll
+    for (int g = 0; g < NG; ++g)
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        base[g][q] = (const char*)a.w.down + (n0 + 16 * g + 8 * q) * row_bytes;
+  };
+  floatx4 acc[NG];
+  auto visit = [&](auto more, int64_t in) {
+    if constexpr (decltype(more)::value) point(in);
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        u32x4 w0, w1;
+        stage_in(stage[wv], lane, ring.w[s][g][0], ring.w[s][g][1]);
+        stage_out(stage[wv], lane, w0, w1);
+#pragma unroll
+        for (int h = 0; h < NH; ++h) S::mma(acc[g], xs[h][s], w0, w1);
+      }
+      if constexpr (decltype(more)::value) ring.load(s, base, st0, nst, row_bytes);
+      __builtin_amdgcn_sched_barrier(0);
     }
-    if (lane == 0) {
-      if (a.residual) y += wide((const OT*)a.residual + i);
-      narrow((OT*)a.out + i, y);
+  };
+  point(i0);
+#pragma unroll
+  for (int s = 0; s < NS; ++s) ring.load(s, base, st0, nst, row_bytes);
+  int par = 0;
+  int64_t have = -1;
+  for (int64_t i = i0; i < i1; ++i) {
+    const int64_t uc = i / upc;
+    if (uc != have) load_h(have = uc);
+#pragma unroll
+    for (int g = 0; g < NG; ++g) acc[g] = floatx4{0.f, 0.f, 0.f, 0.f};
+    if (i + 1 == i1)
+      visit(std::false_type{}, 0);
+    else
+      visit(std::true_type{}, i + 1);
+#pragma unroll
+    for (int g = 0; g < NG; ++g) red_put(red[par] + (wv * NG + g) * kRedWave, acc[g]);
+    __syncthreads();
+    const int half = tid >> 8, g = NG == 1 ? 0 : half;
+    if (NG == 2 || half == par) {
+      const int m = (tid >> 4) & 15, u = (int)(uc / a.chunks);
+      const int n = (int)(i % upc) * (16 * NG) + 16 * g + (tid & 15);
+      const uint32_t mask = r.mask[u];
+      if ((mask >> m) & 1u) {
+        float v = red_get(red[par] + g * kRedWave, NG * kRedWave, m, tid & 15);
+        if (sizeof(WT) == 1) v *= a.w.s_down[(int64_t)r.expert[u] * a.d + n];
+        const int64_t row = r.row0[u] + __popc(mask & ((1u << m) - 1));
+        a.part[(row * a.chunks + uc % a.chunks) * a.d + n] = v;
+      }
     }
+    par ^= 1;
   }
+}
+
+// y_t = sum over slots of w (sum over chunks), the shared expert, the residual.
+template <typename OT>
+__global__ __launch_bounds__(256) void few_join_kernel(FewArgs a) {
+  const FewRoute& r = *a.route;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= (int64_t)a.T * a.d) return;
+  const int t = (int)(i / a.d), n = (int)(i % a.d);
+  float y = 0.0f;
+  for (int j = 0; j <= a.k; ++j) {
+    const int row = r.row[t][j];
+    if (row < 0) continue;
+    const float* p = a.part + (int64_t)row * a.chunks * a.d + n;
+    float s = 0.0f;
+    for (int c = 0; c < a.chunks; ++c) s += p[(int64_t)c * a.d];
+    y += j < a.k ? r.w[t][j] * s : s;
+  }
+  if (a.residual) y += wide((const OT*)a.residual + i);
+  narrow((OT*)a.out + i, y);
 }
 
 // ------------------------------------------------------------------ host
 struct FewWorkspace {
   float* logits;
-  float* H;
+  FewRoute* route;
+  void* H;
+  bf16_t* Hlo;
+  float* part;
   size_t bytes;
 };
+
+// Elements of F in a chunk of the down products: a wave's NS steps times the waves.
+constexpr int kDownSteps = 4;
+static int64_t down_chunks(const moe_desc_t& d, bool fp8) {
+  const int sk = fp8 ? Stream<uint8_t>::SK
+                     : d.dtype == MOE_DTYPE_F32 ? Stream<float>::SK : Stream<bf16_t>::SK;
+  const int ns = fp8 ? kDownSteps / 2 : kDownSteps;
+  return ceil_div(d.d_ff, (int64_t)sk * ns * kFewWaves);
+}
 
 static FewWorkspace carve_few(const moe_desc_t& d, void* base) {
   size_t off = 0;
@@ -263,8 +497,13 @@ static FewWorkspace carve_few(const moe_desc_t& d, void* base) {
     return r;
   };
   FewWorkspace w{};
+  const int64_t rows = d.T * d.top_k + d.n_shared * d.T;
   w.logits = (float*)take(d.T * d.n_experts * 4);
-  w.H = (float*)take((d.T * d.top_k + d.n_shared * d.T) * d.d_ff * 4);
+  w.route = (FewRoute*)take(sizeof(FewRoute));
+  w.H = take(rows * d.d_ff * (d.dtype == MOE_DTYPE_F32 ? 4 : 2));
+  w.Hlo = (bf16_t*)take(d.dtype == MOE_DTYPE_F32 ? 0 : rows * d.d_ff * 2);
+  // the 8-bit form has the same or fewer chunks
+  w.part = (float*)take(rows * down_chunks(d, false) * d.d_model * 4);
   w.bytes = off;
   return w;
 }
@@ -275,13 +514,43 @@ static moe_status_t validate_few(const moe_desc_t* d) {
   return d->T > kFew ? MOE_E_UNSUPPORTED : MOE_OK;
 }
 
-template <typename XT, typename WT, typename OT>
+template <typename WT, int NS, int R, int NG>
+static void launch_gate_up_few(const FewArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL((few_gate_up_kernel<WT, NS, R, NG>), dim3(device_cu_count()), dim3(kFewThreads),
+                     0, s, a);
+}
+
+template <typename WT, typename OT>
 static hipError_t launch_few(const FewArgs& a, hipStream_t s) {
-  const int grid = 4 * device_cu_count();
-  hipLaunchKernelGGL(few_logits_kernel<XT>, dim3((unsigned)ceil_div(a.T * a.E, 4)), dim3(256), 0,
-                     s, a);
-  hipLaunchKernelGGL((few_gate_up_kernel<XT, WT>), dim3(grid), dim3(kFewThreads), 0, s, a);
-  hipLaunchKernelGGL((few_down_kernel<WT, OT>), dim3(grid), dim3(kFewThreads), 0, s, a);
+  typedef typename Stream<WT>::X XT;
+  const int per = (int)ceil_div(ceil_div(a.d, Stream<WT>::SK), kFewWaves);   // steps per wave
+  hipLaunchKernelGGL(few_logits_kernel<XT>, dim3((unsigned)ceil_div(a.E, 16)), dim3(kFewThreads),
+                     0, s, a);
+  if constexpr (sizeof(WT) == 1) {
+    if (per <= 1)
+      launch_gate_up_few<WT, 1, 1, 2>(a, s);
+    else if (per <= 2)
+      launch_gate_up_few<WT, 2, 2, 2>(a, s);
+    else if (per <= 4)
+      launch_gate_up_few<WT, 4, 4, 2>(a, s);
+    else
+      launch_gate_up_few<WT, 8, 4, 1>(a, s);
+    hipLaunchKernelGGL((few_down_kernel<WT, kDownSteps / 2, 2>), dim3(device_cu_count()),
+                       dim3(kFewThreads), 0, s, a);
+  } else {
+    if (per <= 2)
+      launch_gate_up_few<WT, 2, 2, 1>(a, s);
+    else if (per <= 4)
+      launch_gate_up_few<WT, 4, 4, 1>(a, s);
+    else if (per <= 8)
+      launch_gate_up_few<WT, 8, 8, 1>(a, s);
+    else
+      launch_gate_up_few<WT, 14, 7, 1>(a, s);
+    hipLaunchKernelGGL((few_down_kernel<WT, kDownSteps, 1>), dim3(device_cu_count()),
+                       dim3(kFewThreads), 0, s, a);
+  }
+  hipLaunchKernelGGL(few_join_kernel<OT>, dim3((unsigned)ceil_div((int64_t)a.T * a.d, 256)),
+                     dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
@@ -324,22 +593,26 @@ static moe_status_t few_impl(const moe_desc_t* desc, const void* x, const void* 
                   f,
                   p,
                   w.logits,
+                  w.route,
                   w.H,
+                  w.Hlo,
+                  w.part,
                   (int)d.T,
                   (int)d.d_model,
                   (int)d.n_experts,
                   (int)d.d_ff,
                   (int)d.top_k,
                   (int)d.n_shared,
-                  (int)capacity_of(d)};
+                  (int)capacity_of(d),
+                  (int)down_chunks(d, ew.fp8)};
   const bool of32 = d.out_dtype == MOE_DTYPE_F32;
   hipError_t e;
   if (ew.fp8)
-    e = of32 ? launch_few<bf16_t, uint8_t, float>(a, s) : launch_few<bf16_t, uint8_t, bf16_t>(a, s);
+    e = of32 ? launch_few<uint8_t, float>(a, s) : launch_few<uint8_t, bf16_t>(a, s);
   else if (d.dtype == MOE_DTYPE_F32)
-    e = of32 ? launch_few<float, float, float>(a, s) : launch_few<float, float, bf16_t>(a, s);
+    e = of32 ? launch_few<float, float>(a, s) : launch_few<float, bf16_t>(a, s);
   else
-    e = of32 ? launch_few<bf16_t, bf16_t, float>(a, s) : launch_few<bf16_t, bf16_t, bf16_t>(a, s);
+    e = of32 ? launch_few<bf16_t, float>(a, s) : launch_few<bf16_t, bf16_t>(a, s);
   return e == hipSuccess ? MOE_OK : MOE_E_HIP;
 }
 

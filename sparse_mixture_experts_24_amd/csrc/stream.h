@@ -1,0 +1,173 @@
+// Weight rows streamed once through a workgroup against at most 16 token rows.
+//
+// With so few token rows a product reads far more weight bytes than it computes on (16 x 2
+// operations for 2 bytes of bf16 at most, where the matrix cores do some 400 per byte of
+// HBM), so everything here serves the stream: 16 weight rows at a time, the reduction
+// dimension split over the 8 waves of a workgroup, each wave with several KB of loads in
+// flight, and MFMA 16x16 tiles whose cost does not show.
+//
+// A step is 128 bytes of each of the 16 rows (SK elements); wave w takes steps w, w + 8, ...
+// so the workgroup reads 1 KB runs of a row.  A step is loaded with 8 lanes per 128-byte
+// segment (a lane per row, as the MFMA operand has it, would run the load path at a quarter
+// of its rate) and put into operand order through a wave-private LDS buffer: 16-byte chunk
+// c of row r at position c ^ ((r / 2) % 8), conflict-free both ways.  Lane (row r, group g)
+// then holds chunks 2 g and 2 g + 1 of its row; token operands use the same k order.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "moe_internal.h"
+
+namespace moe {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float floatx4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kStreamThreads = 512, kStreamWaves = kStreamThreads / 64;
+constexpr int kStepBytes = 128;            // of each row
+constexpr int kStageBytes = 16 * kStepBytes;   // a wave's LDS buffer
+
+// 8 e4m3 codes (bytes of lo, then hi) -> 8 bf16 operands, exactly.
+__device__ __forceinline__ bf16x8 widen_e4m3(uint32_t lo, uint32_t hi) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)lo, 1.0f, false);
+  const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)lo, 1.0f, true);
+  const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)hi, 1.0f, false);
+  const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)hi, 1.0f, true);
+  return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+// One lane's token operand of a step, and the product with the staged weights.
+//   XR  16-byte registers of the operand; register i holds the elements from
+//       k_of(g, i) on (8 bf16 or 4 floats)
+template <typename WT>
+struct Stream;
+
+template <>
+struct Stream<bf16_t> {
+  static constexpr int SK = 64, XR = 2, XE = 8;
+  typedef bf16_t X;
+  __device__ static int k_of(int g, int i) { return 16 * g + 8 * i; }
+  __device__ static void mma(floatx4& acc, const u32x4* x, u32x4 w0, u32x4 w1) {
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x[0]),
+                                                  __builtin_bit_cast(bf16x8, w0), acc, 0, 0, 0);
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x[1]),
+                                                  __builtin_bit_cast(bf16x8, w1), acc, 0, 0, 0);
+  }
+};
+
+template <>
+struct Stream<uint8_t> {
+  static constexpr int SK = 128, XR = 4, XE = 8;
+  typedef bf16_t X;
+  __device__ static int k_of(int g, int i) { return 32 * g + 8 * i; }
+  __device__ static void mma(floatx4& acc, const u32x4* x, u32x4 w0, u32x4 w1) {
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x[0]),
+                                                  widen_e4m3(w0[0], w0[1]), acc, 0, 0, 0);
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x[1]),
+                                                  widen_e4m3(w0[2], w0[3]), acc, 0, 0, 0);
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x[2]),
+                                                  widen_e4m3(w1[0], w1[1]), acc, 0, 0, 0);
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x[3]),
+                                                  widen_e4m3(w1[2], w1[3]), acc, 0, 0, 0);
+  }
+};
+
+template <>
+struct Stream<float> {
+  static constexpr int SK = 32, XR = 2, XE = 4;
+  typedef float X;
+  __device__ static int k_of(int g, int i) { return 8 * g + 4 * i; }
+  __device__ static void mma(floatx4& acc, const u32x4* x, u32x4 w0, u32x4 w1) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      acc = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(x[0][i]),
+                                                 __uint_as_float(w0[i]), acc, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      acc = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(x[1][i]),
+                                                 __uint_as_float(w1[i]), acc, 0, 0, 0);
+  }
+};
+
+// Puts a step's two loads (rows lane / 8 and 8 + lane / 8, chunk lane % 8) into operand
+// order.  The buffer belongs to the wave and LDS operations of a wave run in order, so
+// neither call needs a barrier.
+__device__ __forceinline__ void stage_in(char* buf, int lane, u32x4 a, u32x4 b) {
+  const int r = lane >> 3, c = lane & 7;
+  *reinterpret_cast<u32x4*>(buf + r * kStepBytes + 16 * (c ^ (r >> 1))) = a;
+  *reinterpret_cast<u32x4*>(buf + (r + 8) * kStepBytes + 16 * (c ^ ((r + 8) >> 1))) = b;
+}
+__device__ __forceinline__ void stage_out(const char* buf, int lane, u32x4& w0, u32x4& w1) {
+  const int r = lane & 15, g = lane >> 4;
+  w0 = *reinterpret_cast<const u32x4*>(buf + r * kStepBytes + 16 * ((2 * g) ^ (r >> 1)));
+  w1 = *reinterpret_cast<const u32x4*>(buf + r * kStepBytes + 16 * ((2 * g + 1) ^ (r >> 1)));
+}
+
+// The wave's part of one product over whole rows: w_at(i, chunk byte) gives the address of
+// load i (rows lane / 8, 8 + lane / 8) at a byte of the row, x_at(k) the lane's token operand
+// at element k (or nullptr: zero).  R steps are in flight; past the wave's last step the
+// loads repeat it (cache hits, never used).  Elements from K on are zero in the token operand
+// and some valid element of the row in the weights.
+template <typename WT, int R, typename WAt, typename XAt>
+__device__ __forceinline__ void stream_rows(floatx4& acc, char* buf, int K, WAt w_at, XAt x_at) {
+  typedef Stream<WT> S;
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, g = lane >> 4;
+  const int nst = (K + S::SK - 1) / S::SK;
+  const int nj = (nst - wv + kStreamWaves - 1) / kStreamWaves;
+  if (nj <= 0) return;
+  const int row_bytes = K * (int)sizeof(WT);
+  u32x4 w[R][2], x[R][S::XR];
+  auto load = [&](int q, int j) {
+    const int st = wv + kStreamWaves * min(j, nj - 1);
+    const int byte = min(st * kStepBytes + 16 * (lane & 7), row_bytes - 16);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) w[q][i] = *reinterpret_cast<const u32x4*>(w_at(i, byte));
+#pragma unroll
+    for (int i = 0; i < S::XR; ++i) {
+      const int k = st * S::SK + S::k_of(g, i);
+      const auto* p = k < K ? x_at(k) : nullptr;
+      x[q][i] = p ? *reinterpret_cast<const u32x4*>(p) : u32x4{0, 0, 0, 0};
+    }
+  };
+  auto use = [&](int q) {
+    u32x4 w0, w1;
+    stage_in(buf, lane, w[q][0], w[q][1]);
+    stage_out(buf, lane, w0, w1);
+    S::mma(acc, x[q], w0, w1);
+  };
+#pragma unroll
+  for (int q = 0; q < R - 1; ++q) load(q, q);
+  int j0 = 0;
+  for (; j0 + R <= nj; j0 += R) {
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+      load((q + R - 1) % R, j0 + q + R - 1);
+      __builtin_amdgcn_sched_barrier(0);   // the loads stay ahead of the products
+      use(q);
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < R - 1; ++q)
+    if (j0 + q < nj) use(q);
+}
+
+// The waves' 16 x 16 partial products, summed in wave order.  Row stride 20 floats: the four
+// lane groups of a store hit different banks.
+constexpr int kRedLd = 20, kRedWave = 16 * kRedLd;
+__device__ __forceinline__ void red_put(float* red, const floatx4& acc) {
+  const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) red[(4 * g + i) * kRedLd + n] = acc[i];
+}
+// Sum of element (m, n) over the waves; red_stride floats from wave to wave.
+__device__ __forceinline__ float red_get(const float* red, int red_stride, int m, int n) {
+  float v = red[m * kRedLd + n];
+#pragma unroll
+  for (int q = 1; q < kStreamWaves; ++q) v += red[q * red_stride + m * kRedLd + n];
+  return v;
+}
+
+}  // namespace moe
