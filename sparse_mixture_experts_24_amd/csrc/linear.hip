@@ -5,7 +5,10 @@
 // whose place a sparse layer takes (SwiGLU: the gated form with SiLU, then the plain form).
 #include <math.h>
 
+#include <atomic>
+
 #include "moe_internal.h"
+#include "stream.h"
 
 namespace moe {
 
@@ -18,6 +21,7 @@ struct LinearArgs {
   void* out;
   int64_t ldx, ldw, ldr, ldo;
   int M, N, K, act;
+  bool out_f32, wide_rows;
 };
 
 __device__ inline float act_f(float z, int act) {
@@ -31,90 +35,392 @@ __device__ inline float act_f(float z, int act) {
   }
 }
 
-__device__ inline float load_f(const float* p) { return *p; }
-__device__ inline float load_f(const bf16_t* p) { return bf16_to_f32(*p); }
-__device__ inline float load_f(const uint8_t* p) {
-  return __builtin_amdgcn_cvt_f32_fp8((int)*p, 0);
+__device__ inline float scaled(float v, const float* scale, int n) {
+  return scale ? v * scale[n] : v;
 }
-__device__ inline void store_f(float* p, float v) { *p = v; }
-__device__ inline void store_f(bf16_t* p, float v) { *p = f32_to_bf16(v); }
+__device__ inline float biased(float v, const float* bias, int n) {
+  return bias ? v + bias[n] : v;
+}
+__device__ inline float load_out(const LinearArgs& a, const void* base, int64_t i) {
+  return a.out_f32 ? ((const float*)base)[i] : bf16_to_f32(((const bf16_t*)base)[i]);
+}
+__device__ inline void store_out(const LinearArgs& a, int64_t i, float v) {
+  if (a.out_f32)
+    ((float*)a.out)[i] = v;
+  else
+    ((bf16_t*)a.out)[i] = f32_to_bf16(v);
+}
 
-// 64 x 64 output tile, 16-wide K steps through LDS, 4 x 4 sums per thread.
-template <typename XT, typename WT, typename OT, bool GATED>
-__global__ __launch_bounds__(256) void linear_tile_kernel(LinearArgs a) {
-  constexpr int NW = GATED ? 2 : 1;
-  __shared__ float xs[16][65];
-  __shared__ float ws[NW][16][65];
-  const int tiles_n = (a.N + 63) / 64;
-  const int m0 = (int)(blockIdx.x / tiles_n) * 64, n0 = (int)(blockIdx.x % tiles_n) * 64;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const XT* x = (const XT*)a.x;
-  float acc[NW][4][4] = {};
-  for (int k0 = 0; k0 < a.K; k0 += 16) {
-    for (int i = threadIdx.x; i < 64 * 16; i += 256) {
-      const int r = i >> 4, k = k0 + (i & 15);
-      xs[i & 15][r] = (m0 + r < a.M && k < a.K) ? load_f(x + (m0 + r) * a.ldx + k) : 0.0f;
+// Finishes columns n .. n + 7 (below N) of row m from their sums.
+template <bool GATED>
+__device__ __forceinline__ void finish8(const LinearArgs& a, int m, int n, const float* zs,
+                                        const float* us) {
+  const int64_t o = m * a.ldo + n, ro = m * a.ldr + n;
+  const int cnt = min(8, a.N - n);
+  float v[8];
 #pragma unroll
-      for (int q = 0; q < NW; ++q)
-        ws[q][i & 15][r] = (n0 + r < a.N && k < a.K)
-                               ? load_f((const WT*)a.W[q] + (n0 + r) * a.ldw + k) : 0.0f;
+  for (int i = 0; i < 8; ++i) {
+    const int c = n + min(i, cnt - 1);
+    v[i] = act_f(biased(scaled(zs[i], a.scale[0], c), a.bias[0], c), a.act);
+    if constexpr (GATED) v[i] *= biased(scaled(us[i], a.scale[1], c), a.bias[1], c);
+  }
+  if (a.wide_rows && cnt == 8) {   // rows of out and residual 16-byte aligned
+    if (a.out_f32) {
+      float4 p = make_float4(0.f, 0.f, 0.f, 0.f), q = p;
+      if (a.residual) {
+        p = *reinterpret_cast<const float4*>((const float*)a.residual + ro);
+        q = *reinterpret_cast<const float4*>((const float*)a.residual + ro + 4);
+      }
+      float* out = (float*)a.out + o;
+      *reinterpret_cast<float4*>(out) = make_float4(v[0] + p.x, v[1] + p.y, v[2] + p.z, v[3] + p.w);
+      *reinterpret_cast<float4*>(out + 4) =
+          make_float4(v[4] + q.x, v[5] + q.y, v[6] + q.z, v[7] + q.w);
+    } else {
+      u32x4 r = {0, 0, 0, 0};
+      if (a.residual) r = *reinterpret_cast<const u32x4*>((const bf16_t*)a.residual + ro);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        r[i] = (uint32_t)f32_to_bf16(v[2 * i] + __uint_as_float(r[i] << 16)) |
+               (uint32_t)f32_to_bf16(v[2 * i + 1] + __uint_as_float(r[i] & 0xFFFF0000u)) << 16;
+      *reinterpret_cast<u32x4*>((bf16_t*)a.out + o) = r;
     }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < 16; ++k)
-#pragma unroll
-      for (int q = 0; q < NW; ++q)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            acc[q][i][j] = fmaf(xs[k][ty + 16 * i], ws[q][k][tx + 16 * j], acc[q][i][j]);
-    __syncthreads();
+    return;
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int m = m0 + ty + 16 * i, n = n0 + tx + 16 * j;
-      if (m >= a.M || n >= a.N) continue;
-      float z[NW];
-#pragma unroll
-      for (int q = 0; q < NW; ++q) {
-        z[q] = acc[q][i][j];
-        if (a.scale[q]) z[q] *= a.scale[q][n];
-        if (a.bias[q]) z[q] += a.bias[q][n];
-      }
-      float v = act_f(z[0], a.act);
-      if constexpr (GATED) v *= z[1];
-      if (a.residual) v += load_f((const OT*)a.residual + m * a.ldr + n);
-      store_f((OT*)a.out + m * a.ldo + n, v);
-    }
+  for (int i = 0; i < 8; ++i)
+    if (i < cnt) store_out(a, o + i, a.residual ? v[i] + load_out(a, a.residual, ro + i) : v[i]);
 }
 
-template <typename XT, typename WT, typename OT>
-static hipError_t launch_tiles(const LinearArgs& a, bool gated, hipStream_t s) {
-  const int64_t grid = ceil_div(a.M, 64) * ceil_div(a.N, 64);
-  if (gated)
-    hipLaunchKernelGGL((linear_tile_kernel<XT, WT, OT, true>), dim3((unsigned)grid), dim3(256), 0,
-                       s, a);
-  else
-    hipLaunchKernelGGL((linear_tile_kernel<XT, WT, OT, false>), dim3((unsigned)grid), dim3(256),
-                       0, s, a);
+// ------------------------------------------------------------------ at most 16 rows
+// A workgroup streams 16 weight rows (gated: 8 gate rows and the 8 matching up rows) over the
+// whole of K, split over its waves.
+template <typename WT, bool GATED>
+__global__ __launch_bounds__(kStreamThreads) void linear_rows_kernel(LinearArgs a) {
+  typedef Stream<WT> S;
+  typedef typename S::X XT;
+  __shared__ __align__(16) char stage[kStreamWaves][kStageBytes];
+  __shared__ float red[kStreamWaves * kRedWave];
+  constexpr int COLS = GATED ? 8 : 16;
+  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, t = lane & 15;
+  const int n0 = blockIdx.x * COLS;
+  const char* row[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    row[i] = (const char*)a.W[GATED ? i : 0] +
+             (int64_t)min(n0 + (GATED ? 0 : 8 * i) + (lane >> 3), a.N - 1) * a.ldw * (int)sizeof(WT);
+  const XT* x = (const XT*)a.x + (int64_t)min(t, a.M - 1) * a.ldx;
+  floatx4 acc = {0.f, 0.f, 0.f, 0.f};
+  stream_rows<WT, 8>(acc, stage[wv], a.K, [&](int i, int byte) { return row[i] + byte; },
+                     [&](int k) { return t < a.M ? x + k : nullptr; });
+  red_put(red + wv * kRedWave, acc);
+  __syncthreads();
+  if (tid >= 256) return;
+  const int m = tid >> 4, q = tid & 15;
+  const int n = n0 + (GATED ? q & 7 : q), nc = min(n, a.N - 1), mat = GATED ? q >> 3 : 0;
+  float v = biased(scaled(red_get(red, kRedWave, m, q), a.scale[mat], nc), a.bias[mat], nc);
+  if constexpr (GATED) {
+    const float up = __shfl_xor(v, 8, 64);
+    v = act_f(v, a.act) * up;
+    if (q >= 8) return;
+  } else {
+    v = act_f(v, a.act);
+  }
+  if (m >= a.M || n >= a.N) return;
+  if (a.residual) v += load_out(a, a.residual, m * a.ldr + n);
+  store_out(a, m * a.ldo + n, v);
+}
+
+// ------------------------------------------------------------------ MFMA tiles
+// A tile of 64 MB rows by 64 NB weight rows per workgroup of 4 waves (2 x 2), a wave holding
+// MB x NB blocks of 32 x 32 sums.  K runs in steps of 128 bytes of an x row through two LDS
+// stages that global loads fill directly (no registers between).  A step is four slices of
+// one k range per MFMA block; the operands of slice s + 1 are read from LDS while the MFMAs
+// of slice s run.  The barrier that frees a stage stands before the last slice's MFMAs,
+// whose operands are in registers by then, so the other stage's first reads and the loads
+// of the step after next run under them.
+//   LDS rows are 128 bytes (8-bit weights: 64), the 16-byte chunk c of row r at position
+// c ^ (r % 8) (8-bit: c ^ (r / 2 % 4)), applied to the addresses that the lanes load from:
+// a direct load puts lane l's 16 bytes at 16 l.  The operand reads of 8 neighbouring rows
+// then take 8 different positions.
+//   Gated: the weight blocks of a wave alternate gate and up rows of the same columns, so
+// act(g) * u is formed in registers.
+typedef float floatx16 __attribute__((ext_vector_type(16)));
+
+// 16 bytes per lane from g straight into LDS at lds + 16 lane (lds: byte offset, uniform).
+// The compiler does not count this load: wait with wait_loads() before the barrier after
+// which the data is read.
+__device__ __forceinline__ void load_to_lds(const void* g, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
+               :: "v"(g), "s"(lds));   // nothing else here uses m0
+}
+// Every load to LDS has landed, every LDS read of this wave is done, LDS contents are new to
+// the compiler.
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+}
+// Barrier that LDS accesses do not cross.
+__device__ __forceinline__ void stage_barrier() {
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+template <typename WT>
+struct Tile {   // bf16
+  static constexpr int BK = 64, WROW = 128;   // k per step, bytes of a weight row in it
+  typedef bf16_t X;
+  typedef u32x4 WReg;
+  __device__ static void mma(floatx16& acc, u32x4 x, u32x4 w) {
+    acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, x),
+                                                  __builtin_bit_cast(bf16x8, w), acc, 0, 0, 0);
+  }
+  __device__ static u32x4 operand(u32x4 w) { return w; }
+};
+template <>
+struct Tile<uint8_t> {
+  static constexpr int BK = 64, WROW = 64;
+  typedef bf16_t X;
+  typedef uint2 WReg;
+  __device__ static void mma(floatx16& acc, u32x4 x, u32x4 w) { Tile<bf16_t>::mma(acc, x, w); }
+  __device__ static u32x4 operand(uint2 w) {
+    return __builtin_bit_cast(u32x4, widen_e4m3(w.x, w.y));
+  }
+};
+template <>
+struct Tile<float> {
+  static constexpr int BK = 32, WROW = 128;
+  typedef float X;
+  typedef u32x4 WReg;
+  __device__ static void mma(floatx16& acc, u32x4 x, u32x4 w) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)   // lane half h holds k = 4 h + j
+      acc = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(x[j]), __uint_as_float(w[j]), acc,
+                                                 0, 0, 0);
+  }
+  __device__ static u32x4 operand(u32x4 w) { return w; }
+};
+
+constexpr int kXRow = 128;   // bytes of an x row in a stage
+
+template <typename WT, int MB, int NB>
+constexpr int tile_stage_bytes() {
+  return 64 * MB * kXRow + 64 * NB * Tile<WT>::WROW;
+}
+// The epilogue's transpose buffer: 32 rows of a wave's sums, padded by 4 floats.
+template <int NB>
+constexpr int tile_epilogue_ld() {
+  return 32 * NB + 4;
+}
+template <typename WT, int MB, int NB>
+constexpr int tile_lds_bytes() {
+  const int stages = 2 * tile_stage_bytes<WT, MB, NB>();
+  const int epi = 4 * 32 * tile_epilogue_ld<NB>() * 4;
+  return stages > epi ? stages : epi;
+}
+
+// Tile of a workgroup.  Workgroup i runs on XCD i % 8; every XCD takes a run of consecutive
+// tiles, ordered in groups of 8 row tiles so that the tiles an XCD works on at a time share
+// x rows and weight rows in its L2.
+__device__ inline void tile_of(const LinearArgs& a, int tiles_m, int tiles_n, int& tm, int& tn) {
+  const int total = tiles_m * tiles_n, xcd = blockIdx.x & 7, q = total >> 3, rest = total & 7;
+  const int pos = xcd * q + min(xcd, rest) + (int)(blockIdx.x >> 3);
+  const int per = 8 * tiles_n, grp = pos / per, rows = min(8, tiles_m - 8 * grp);
+  tm = 8 * grp + pos % per % rows;
+  tn = pos % per / rows;
+}
+
+template <typename WT, int MB, int NB, bool GATED>
+__global__ __launch_bounds__(256, MB * NB >= 8 ? 1 : 2) void linear_tile_kernel(LinearArgs a) {
+  typedef Tile<WT> TT;
+  typedef typename TT::X XT;
+  static_assert(!GATED || NB % 2 == 0, "gate and up blocks come in pairs");
+  constexpr int BM = 64 * MB, BN = 64 * NB, OUT_N = GATED ? BN / 2 : BN;
+  constexpr int STAGE = tile_stage_bytes<WT, MB, NB>(), XBYTES = BM * kXRow;
+  constexpr bool W8 = sizeof(WT) == 1;
+  constexpr int WRPL = W8 ? 16 : 8;                    // weight rows per load
+  constexpr int NX = BM / 8 / 4, NW = BN / WRPL / 4;   // loads per wave and step
+  extern __shared__ __align__(16) char smem[];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6), wm = w >> 1, wn = w & 1;
+  int tm, tn;
+  tile_of(a, (a.M + BM - 1) / BM, (a.N + OUT_N - 1) / OUT_N, tm, tn);
+  const int m0 = tm * BM, n0 = tn * OUT_N;
+
+  // What this lane loads: rows of the tile (clamped into the matrices) at its chunk.
+  const int xchunk = (lane & 7) ^ (lane >> 3);
+  const int wchunk = W8 ? (lane & 3) ^ ((lane >> 3) & 3) : xchunk;
+  const char* px[NX];
+  const char* pw[NW];
+#pragma unroll
+  for (int i = 0; i < NX; ++i) {
+    const int m = min(m0 + (w * NX + i) * 8 + (lane >> 3), a.M - 1);
+    px[i] = (const char*)a.x + m * a.ldx * (int)sizeof(XT) + 16 * xchunk;
+  }
+#pragma unroll
+  for (int i = 0; i < NW; ++i) {
+    const int j = (w * NW + i) * WRPL + (W8 ? lane >> 2 : lane >> 3);
+    const int mat = GATED ? (j >> 5) & 1 : 0;
+    const int col = GATED ? (j / (32 * NB)) * (16 * NB) + ((j / 32) % NB >> 1) * 32 + (j & 31) : j;
+    pw[i] = (const char*)a.W[mat] + min(n0 + col, a.N - 1) * a.ldw * (int)sizeof(WT) + 16 * wchunk;
+  }
+  const int nk = (a.K + TT::BK - 1) / TT::BK;
+  // Load i of step t into its stage; the last step's chunks past K become zero.
+  auto load = [&](int i, int t) {
+    const bool isx = i < NX;
+    const int q = isx ? i : i - NX;
+    const uint32_t dst = (uint32_t)((t & 1) * STAGE + (isx ? (w * NX + q) * 1024
+                                                           : XBYTES + (w * NW + q) * 1024));
+    const char* src = isx ? px[isx ? q : 0] : pw[isx ? 0 : q];
+    const int k = t * TT::BK + (isx ? xchunk * (16 / (int)sizeof(XT))
+                                    : wchunk * (16 / (int)sizeof(WT)));
+    if (t + 1 < nk || k < a.K)
+      load_to_lds(src, dst);
+    else
+      *reinterpret_cast<u32x4*>(smem + dst + 16 * lane) = u32x4{0, 0, 0, 0};
+    if (isx)
+      px[isx ? q : 0] += kXRow;
+    else
+      pw[isx ? 0 : q] += TT::WROW;
+  };
+
+  // Operand reads: row lane % 32 of a block, lane half = k half of the slice.
+  const int fr = lane & 31, fh = lane >> 5;
+  const int xrd = (wm * 32 * MB + fr) * kXRow, xsw = 16 * (fh ^ (fr & 7));
+  const int wrd = XBYTES + (wn * 32 * NB + fr) * TT::WROW;
+  const int wsw = W8 ? 16 * ((fr >> 1) & 3) : xsw;
+  u32x4 xf[2][MB];
+  typename TT::WReg wf[2][NB];
+  auto read_x = [&](int buf, int mb, int st, int s) {
+    xf[buf][mb] = *reinterpret_cast<const u32x4*>(smem + st * STAGE + xrd + mb * 32 * kXRow +
+                                                  (xsw ^ (32 * s)));
+  };
+  auto read_w = [&](int buf, int nb, int st, int s) {
+    wf[buf][nb] = *reinterpret_cast<const typename TT::WReg*>(
+        smem + st * STAGE + wrd + nb * 32 * TT::WROW + (W8 ? (wsw ^ (16 * s)) + 8 * fh
+                                                           : wsw ^ (32 * s)));
+  };
+  floatx16 acc[MB][NB];
+#pragma unroll
+  for (int i = 0; i < MB; ++i)
+#pragma unroll
+    for (int j = 0; j < NB; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+
+#pragma unroll
+  for (int i = 0; i < NX + NW; ++i) load(i, 0);
+  wait_loads();
+  stage_barrier();
+  if (nk > 1) {
+#pragma unroll
+    for (int i = 0; i < NX + NW; ++i) load(i, 1);
+  }
+#pragma unroll
+  for (int i = 0; i < MB; ++i) read_x(0, i, 0, 0);
+#pragma unroll
+  for (int i = 0; i < NB; ++i) read_w(0, i, 0, 0);
+  for (int t = 0; t < nk; ++t) {
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      const int buf = s & 1, st = s < 3 ? t & 1 : (t + 1) & 1, sn = (s + 1) & 3;
+      if (s == 3) {
+        // stage t is read out by every wave, stage t + 1 has landed
+        wait_loads();
+        stage_barrier();
+      }
+      u32x4 wo[NB];
+#pragma unroll
+      for (int i = 0; i < NB; ++i) wo[i] = TT::operand(wf[buf][i]);
+      // reads of the next slice (past the last step: stale, unused)
+#pragma unroll
+      for (int i = 0; i < MB; ++i) read_x(buf ^ 1, i, st, sn);
+#pragma unroll
+      for (int i = 0; i < NB; ++i) read_w(buf ^ 1, i, st, sn);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < MB; ++i)
+#pragma unroll
+        for (int j = 0; j < NB; ++j) TT::mma(acc[i][j], xf[buf][i], wo[j]);
+      if (s == 3 && t + 2 < nk) {
+#pragma unroll
+        for (int i = 0; i < NX + NW; ++i) load(i, t + 2);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+  wait_loads();
+  stage_barrier();   // the stages are free for the transposes
+
+  // Epilogue, a wave by itself: the sums of 32 rows at a time through LDS, so that a lane
+  // finishes 8 neighbouring columns of a row and rows leave in whole segments.
+  constexpr int LD = tile_epilogue_ld<NB>(), WC = 32 * NB / (GATED ? 2 : 1), PER = WC / 8;
+  float* tr = (float*)smem + w * 32 * LD;
+#pragma unroll
+  for (int i = 0; i < MB; ++i) {
+#pragma unroll
+    for (int j = 0; j < NB; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        tr[(8 * (r >> 2) + 4 * fh + (r & 3)) * LD + 32 * j + fr] = acc[i][j][r];
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll 1
+    for (int e = lane; e < 32 * PER; e += 64) {
+      const int row = e / PER, c = e % PER * 8;
+      const int m = m0 + (wm * MB + i) * 32 + row, n = n0 + wn * WC + c;
+      // gated: the up sums of a 32-column block follow its gate sums
+      const float* z = tr + row * LD + (GATED ? 64 * (c >> 5) + (c & 31) : c);
+      if (m < a.M && n < a.N) finish8<GATED>(a, m, n, z, z + 32);
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  }
+}
+
+// The LDS of a tile kernel is above the default limit: raised once per device and kernel.
+template <typename WT, int MB, int NB, bool GATED>
+static hipError_t run_tiles(const LinearArgs& a, hipStream_t s) {
+  static std::atomic<bool> done[kMaxDevices];
+  constexpr int lds = tile_lds_bytes<WT, MB, NB>();
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices || !done[dev].load(std::memory_order_acquire)) {
+    e = hipFuncSetAttribute((const void*)linear_tile_kernel<WT, MB, NB, GATED>,
+                            hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    if (e != hipSuccess) return e;
+    if (dev >= 0 && dev < kMaxDevices) done[dev].store(true, std::memory_order_release);
+  }
+  const int64_t tiles = ceil_div(a.M, 64 * MB) * ceil_div(a.N, 64 * NB / (GATED ? 2 : 1));
+  hipLaunchKernelGGL((linear_tile_kernel<WT, MB, NB, GATED>), dim3((unsigned)tiles), dim3(256),
+                     lds, s, a);
   return hipGetLastError();
 }
 
-template <typename XT, typename WT>
-static hipError_t launch_linear_o(const moe_linear_desc_t& d, const LinearArgs& a, bool gated,
-                                  hipStream_t s) {
-  return d.out_dtype == MOE_DTYPE_F32 ? launch_tiles<XT, WT, float>(a, gated, s)
-                                      : launch_tiles<XT, WT, bf16_t>(a, gated, s);
+template <typename WT, bool GATED>
+static hipError_t launch_linear_t(const LinearArgs& a, hipStream_t s) {
+  if (a.M <= 16) {
+    hipLaunchKernelGGL((linear_rows_kernel<WT, GATED>),
+                       dim3((unsigned)ceil_div(a.N, GATED ? 8 : 16)), dim3(kStreamThreads), 0, s,
+                       a);
+    return hipGetLastError();
+  }
+  // Largest tile that still gives every CU one; below that, what gives the most.
+  const int64_t cus = device_cu_count(), out = GATED ? 2 : 1;
+  auto tiles = [&](int mb, int nb) { return ceil_div(a.M, 64 * mb) * ceil_div(a.N * out, 64 * nb); };
+  if (tiles(4, 4) >= cus) return run_tiles<WT, 4, 4, GATED>(a, s);
+  if (tiles(4, 2) >= cus) return run_tiles<WT, 4, 2, GATED>(a, s);
+  if (tiles(2, 2) >= cus) return run_tiles<WT, 2, 2, GATED>(a, s);
+  return run_tiles<WT, 1, GATED ? 2 : 1, GATED>(a, s);
+}
+
+template <typename WT>
+static hipError_t launch_linear_w(const LinearArgs& a, bool gated, hipStream_t s) {
+  return gated ? launch_linear_t<WT, true>(a, s) : launch_linear_t<WT, false>(a, s);
 }
 
 static hipError_t launch_linear(const moe_linear_desc_t& d, const LinearArgs& a, bool gated,
                                 bool fp8, hipStream_t s) {
-  if (fp8) return launch_linear_o<bf16_t, uint8_t>(d, a, gated, s);
-  return d.dtype == MOE_DTYPE_F32 ? launch_linear_o<float, float>(d, a, gated, s)
-                                  : launch_linear_o<bf16_t, bf16_t>(d, a, gated, s);
+  if (fp8) return launch_linear_w<uint8_t>(a, gated, s);
+  return d.dtype == MOE_DTYPE_F32 ? launch_linear_w<float>(a, gated, s)
+                                  : launch_linear_w<bf16_t>(a, gated, s);
 }
 
 // ------------------------------------------------------------------ host checks
@@ -154,7 +460,7 @@ static moe_status_t linear_impl(const moe_linear_desc_t* desc, const void* x, co
   const moe_linear_desc_t& d = *desc;
   if (!W0 || (gated && !W1) || (fp8 && (!s0 || (gated && !s1))) || (d.M > 0 && (!x || !out)))
     return MOE_E_NULL;
-  const uintptr_t ob = d.out_dtype == MOE_DTYPE_F32 ? 4 : 2;
+  const int64_t ob = d.out_dtype == MOE_DTYPE_F32 ? 4 : 2;
   if (!aligned_to(x, 16) || !aligned_to(W0, 16) || !aligned_to(W1, 16) || !aligned_to(s0, 4) ||
       !aligned_to(s1, 4) || !aligned_to(b0, 4) || !aligned_to(b1, 4) ||
       !aligned_to(residual, ob) || !aligned_to(out, ob))
@@ -175,7 +481,11 @@ static moe_status_t linear_impl(const moe_linear_desc_t* desc, const void* x, co
                      (int)d.M,
                      (int)d.N,
                      (int)d.K,
-                     d.act};
+                     d.act,
+                     d.out_dtype == MOE_DTYPE_F32,
+                     aligned_to(out, 16) && aligned_to(residual, 16) &&
+                         (d.ldo ? d.ldo : d.N) * ob % 16 == 0 &&
+                         (d.ldr ? d.ldr : d.N) * ob % 16 == 0};
   return launch_linear(d, a, gated, fp8, (hipStream_t)stream) == hipSuccess ? MOE_OK : MOE_E_HIP;
 }
 
