@@ -6,6 +6,7 @@
 #include <math.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "moe_internal.h"
 #include "stream.h"
@@ -262,9 +263,9 @@ __global__ __launch_bounds__(256, MB * NB >= 8 ? 1 : 2) void linear_tile_kernel(
     const int col = GATED ? (j / (32 * NB)) * (16 * NB) + ((j / 32) % NB >> 1) * 32 + (j & 31) : j;
     pw[i] = (const char*)a.W[mat] + min(n0 + col, a.N - 1) * a.ldw * (int)sizeof(WT) + 16 * wchunk;
   }
-  const int nk = (a.K + TT::BK - 1) / TT::BK;
-  // Load i of step t into its stage; the last step's chunks past K become zero.
-  auto load = [&](int i, int t) {
+  const int nk = (a.K + TT::BK - 1) / TT::BK, nfull = a.K / TT::BK;
+  // Load i of step t into its stage; a last step that K does not fill (TAIL) has zeros past K.
+  auto load = [&](auto tail, int i, int t) {
     const bool isx = i < NX;
     const int q = isx ? i : i - NX;
     const uint32_t dst = (uint32_t)((t & 1) * STAGE + (isx ? (w * NX + q) * 1024
@@ -272,7 +273,7 @@ __global__ __launch_bounds__(256, MB * NB >= 8 ? 1 : 2) void linear_tile_kernel(
     const char* src = isx ? px[isx ? q : 0] : pw[isx ? 0 : q];
     const int k = t * TT::BK + (isx ? xchunk * (16 / (int)sizeof(XT))
                                     : wchunk * (16 / (int)sizeof(WT)));
-    if (t + 1 < nk || k < a.K)
+    if (!decltype(tail)::value || k < a.K)
       load_to_lds(src, dst);
     else
       *reinterpret_cast<u32x4*>(smem + dst + 16 * lane) = u32x4{0, 0, 0, 0};
@@ -280,6 +281,15 @@ __global__ __launch_bounds__(256, MB * NB >= 8 ? 1 : 2) void linear_tile_kernel(
       px[isx ? q : 0] += kXRow;
     else
       pw[isx ? 0 : q] += TT::WROW;
+  };
+  auto load_step = [&](int t) {
+    if (t < nfull) {
+#pragma unroll
+      for (int i = 0; i < NX + NW; ++i) load(std::false_type{}, i, t);
+    } else if (t < nk) {
+#pragma unroll
+      for (int i = 0; i < NX + NW; ++i) load(std::true_type{}, i, t);
+    }
   };
 
   // Operand reads: row lane % 32 of a block, lane half = k half of the slice.
@@ -306,19 +316,17 @@ __global__ __launch_bounds__(256, MB * NB >= 8 ? 1 : 2) void linear_tile_kernel(
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
 
-#pragma unroll
-  for (int i = 0; i < NX + NW; ++i) load(i, 0);
+  load_step(0);
   wait_loads();
   stage_barrier();
-  if (nk > 1) {
-#pragma unroll
-    for (int i = 0; i < NX + NW; ++i) load(i, 1);
-  }
+  load_step(1);
 #pragma unroll
   for (int i = 0; i < MB; ++i) read_x(0, i, 0, 0);
 #pragma unroll
   for (int i = 0; i < NB; ++i) read_w(0, i, 0, 0);
-  for (int t = 0; t < nk; ++t) {
+  // Step t.  BODY: step t + 2 is a full one, whose loads go out between the last slice's MFMAs,
+  // as early as its stage is free.
+  auto step = [&](auto body, int t) {
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       const int buf = s & 1, st = s < 3 ? t & 1 : (t + 1) & 1, sn = (s + 1) & 3;
@@ -326,27 +334,42 @@ __global__ __launch_bounds__(256, MB * NB >= 8 ? 1 : 2) void linear_tile_kernel(
         // stage t is read out by every wave, stage t + 1 has landed
         wait_loads();
         stage_barrier();
+        if constexpr (!decltype(body)::value) load_step(t + 2);
       }
       u32x4 wo[NB];
 #pragma unroll
       for (int i = 0; i < NB; ++i) wo[i] = TT::operand(wf[buf][i]);
-      // reads of the next slice (past the last step: stale, unused)
-#pragma unroll
-      for (int i = 0; i < MB; ++i) read_x(buf ^ 1, i, st, sn);
-#pragma unroll
-      for (int i = 0; i < NB; ++i) read_w(buf ^ 1, i, st, sn);
+      // One operand read of the next slice (past the last step: stale, unused) after each
+      // MFMA, in whose shadow it issues.
+      constexpr int B = MB * NB, RD = MB + NB, L = NX + NW, kPerMma = (RD + B - 1) / B;
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int i = 0; i < MB; ++i)
 #pragma unroll
-        for (int j = 0; j < NB; ++j) TT::mma(acc[i][j], xf[buf][i], wo[j]);
-      if (s == 3 && t + 2 < nk) {
+        for (int j = 0; j < NB; ++j) {
+          const int q = i * NB + j;
+          TT::mma(acc[i][j], xf[buf][i], wo[j]);
 #pragma unroll
-        for (int i = 0; i < NX + NW; ++i) load(i, t + 2);
-      }
+          for (int l = q * kPerMma; l < (q + 1 == B ? RD : min((q + 1) * kPerMma, RD)); ++l) {
+            if (l < NB)
+              read_w(buf ^ 1, l < NB ? l : 0, st, sn);
+            else
+              read_x(buf ^ 1, l >= NB ? l - NB : 0, st, sn);
+          }
+          if constexpr (decltype(body)::value) {
+            if (s == 3) {
+#pragma unroll
+              for (int l = q * L / B; l < (q + 1) * L / B; ++l) load(std::false_type{}, l, t + 2);
+            }
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
       __builtin_amdgcn_sched_barrier(0);
     }
-  }
+  };
+  int t = 0;
+  for (; t + 2 < nfull; ++t) step(std::true_type{}, t);
+  for (; t < nk; ++t) step(std::false_type{}, t);
   wait_loads();
   stage_barrier();   // the stages are free for the transposes
 
