@@ -36,6 +36,21 @@ __device__ inline float act_f(float z, int act) {
   }
 }
 
+__device__ __forceinline__ void act8(float* z, int act) {
+  switch (act) {
+#define MOE_ACT8(A)                                           \
+  case A:                                                     \
+    _Pragma("unroll") for (int i = 0; i < 8; ++i) z[i] = act_f(z[i], A); \
+    break;
+    MOE_ACT8(MOE_ACT_RELU)
+    MOE_ACT8(MOE_ACT_GELU)
+    MOE_ACT8(MOE_ACT_GELU_TANH)
+    MOE_ACT8(MOE_ACT_SILU)
+#undef MOE_ACT8
+    default: break;
+  }
+}
+
 __device__ inline float scaled(float v, const float* scale, int n) {
   return scale ? v * scale[n] : v;
 }
@@ -52,44 +67,47 @@ __device__ inline void store_out(const LinearArgs& a, int64_t i, float v) {
     ((bf16_t*)a.out)[i] = f32_to_bf16(v);
 }
 
-// Finishes columns n .. n + 7 (below N) of row m from their sums.
-template <bool GATED>
-__device__ __forceinline__ void finish8(const LinearArgs& a, int m, int n, const float* zs,
-                                        const float* us) {
-  const int64_t o = m * a.ldo + n, ro = m * a.ldr + n;
-  const int cnt = min(8, a.N - n);
-  float v[8];
+// What a lane needs of its 8 neighbouring columns n .. n + 7 (those past N: column N - 1).
+struct Columns {
+  float scale[8], bias[8];
+  __device__ __forceinline__ void load(const LinearArgs& a, int mat, int n) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int c = n + min(i, cnt - 1);
-    v[i] = act_f(biased(scaled(zs[i], a.scale[0], c), a.bias[0], c), a.act);
-    if constexpr (GATED) v[i] *= biased(scaled(us[i], a.scale[1], c), a.bias[1], c);
-  }
-  if (a.wide_rows && cnt == 8) {   // rows of out and residual 16-byte aligned
-    if (a.out_f32) {
-      float4 p = make_float4(0.f, 0.f, 0.f, 0.f), q = p;
-      if (a.residual) {
-        p = *reinterpret_cast<const float4*>((const float*)a.residual + ro);
-        q = *reinterpret_cast<const float4*>((const float*)a.residual + ro + 4);
-      }
-      float* out = (float*)a.out + o;
-      *reinterpret_cast<float4*>(out) = make_float4(v[0] + p.x, v[1] + p.y, v[2] + p.z, v[3] + p.w);
-      *reinterpret_cast<float4*>(out + 4) =
-          make_float4(v[4] + q.x, v[5] + q.y, v[6] + q.z, v[7] + q.w);
-    } else {
-      u32x4 r = {0, 0, 0, 0};
-      if (a.residual) r = *reinterpret_cast<const u32x4*>((const bf16_t*)a.residual + ro);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        r[i] = (uint32_t)f32_to_bf16(v[2 * i] + __uint_as_float(r[i] << 16)) |
-               (uint32_t)f32_to_bf16(v[2 * i + 1] + __uint_as_float(r[i] & 0xFFFF0000u)) << 16;
-      *reinterpret_cast<u32x4*>((bf16_t*)a.out + o) = r;
+    for (int i = 0; i < 8; ++i) {
+      const int c = min(n + i, a.N - 1);
+      scale[i] = a.scale[mat] ? a.scale[mat][c] : 1.0f;
+      bias[i] = a.bias[mat] ? a.bias[mat][c] : 0.0f;
     }
-    return;
   }
+};
+// The residual's 8 values at element i, as they are stored (wide rows only).
+struct Residual8 {
+  u32x4 lo, hi;
+  __device__ __forceinline__ void load(const LinearArgs& a, int64_t i) {
+    if (a.out_f32) {
+      lo = *reinterpret_cast<const u32x4*>((const float*)a.residual + i);
+      hi = *reinterpret_cast<const u32x4*>((const float*)a.residual + i + 4);
+    } else {
+      lo = *reinterpret_cast<const u32x4*>((const bf16_t*)a.residual + i);
+    }
+  }
+  __device__ __forceinline__ float get(const LinearArgs& a, int i) const {
+    if (a.out_f32) return __uint_as_float(i < 4 ? lo[i & 3] : hi[i & 3]);
+    return __uint_as_float(i & 1 ? lo[i >> 1] & 0xFFFF0000u : lo[i >> 1] << 16);
+  }
+};
+// Stores 8 neighbouring values (wide rows).
+__device__ __forceinline__ void store8(const LinearArgs& a, int64_t i, const float* v) {
+  if (a.out_f32) {
+    float* out = (float*)a.out + i;
+    *reinterpret_cast<float4*>(out) = make_float4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<float4*>(out + 4) = make_float4(v[4], v[5], v[6], v[7]);
+  } else {
+    u32x4 r;
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (i < cnt) store_out(a, o + i, a.residual ? v[i] + load_out(a, a.residual, ro + i) : v[i]);
+    for (int q = 0; q < 4; ++q)
+      r[q] = (uint32_t)f32_to_bf16(v[2 * q]) | (uint32_t)f32_to_bf16(v[2 * q + 1]) << 16;
+    *reinterpret_cast<u32x4*>((bf16_t*)a.out + i) = r;
+  }
 }
 
 // ------------------------------------------------------------------ at most 16 rows
@@ -374,24 +392,70 @@ __global__ __launch_bounds__(256, MB * NB >= 8 ? 1 : 2) void linear_tile_kernel(
   stage_barrier();   // the stages are free for the transposes
 
   // Epilogue, a wave by itself: the sums of 32 rows at a time through LDS, so that a lane
-  // finishes 8 neighbouring columns of a row and rows leave in whole segments.
+  // finishes 8 neighbouring columns of a row and rows leave in whole segments.  The lane's
+  // columns are the same in every row; the sums and residual of its next row are read
+  // while one is finished.  One copy of the code for all MB blocks (only the LDS writes
+  // name the accumulators), as it holds every activation.
   constexpr int LD = tile_epilogue_ld<NB>(), WC = 32 * NB / (GATED ? 2 : 1), PER = WC / 8;
+  constexpr int STEP = 64 / PER;   // rows a wave finishes at a time
   float* tr = (float*)smem + w * 32 * LD;
-#pragma unroll
+  const int c = lane % PER * 8, n = n0 + wn * WC + c, row0 = lane / PER;
+  const float* z = tr + (GATED ? 64 * (c >> 5) + (c & 31) : c);   // gated: up sums 32 further
+  Columns cg, cu;
+  cg.load(a, 0, n);
+  if constexpr (GATED) cu.load(a, 1, n);
+  const bool wide = a.wide_rows && n + 8 <= a.N;
+#pragma unroll 1
   for (int i = 0; i < MB; ++i) {
 #pragma unroll
-    for (int j = 0; j < NB; ++j)
+    for (int q = 0; q < MB; ++q)
+      if (q == i) {
 #pragma unroll
-      for (int r = 0; r < 16; ++r)
-        tr[(8 * (r >> 2) + 4 * fh + (r & 3)) * LD + 32 * j + fr] = acc[i][j][r];
+        for (int j = 0; j < NB; ++j)
+#pragma unroll
+          for (int r = 0; r < 16; ++r)
+            tr[(8 * (r >> 2) + 4 * fh + (r & 3)) * LD + 32 * j + fr] = acc[q][j][r];
+      }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    const int mw = m0 + (wm * MB + i) * 32 + row0;
+    float zg[8], zu[8];
+    Residual8 res;
+    auto fetch = [&](int row) {   // row of the 32, from row0
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        zg[e] = z[(row0 + row) * LD + e];
+        if constexpr (GATED) zu[e] = z[(row0 + row) * LD + 32 + e];
+      }
+      if (a.residual && wide && mw + row < a.M) res.load(a, (mw + row) * a.ldr + n);
+    };
+    fetch(0);
 #pragma unroll 1
-    for (int e = lane; e < 32 * PER; e += 64) {
-      const int row = e / PER, c = e % PER * 8;
-      const int m = m0 + (wm * MB + i) * 32 + row, n = n0 + wn * WC + c;
-      // gated: the up sums of a 32-column block follow its gate sums
-      const float* z = tr + row * LD + (GATED ? 64 * (c >> 5) + (c & 31) : c);
-      if (m < a.M && n < a.N) finish8<GATED>(a, m, n, z, z + 32);
+    for (int row = 0; row < 32; row += STEP) {
+      float v[8], u[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        v[e] = fmaf(zg[e], cg.scale[e], cg.bias[e]);
+        if constexpr (GATED) u[e] = fmaf(zu[e], cu.scale[e], cu.bias[e]);
+      }
+      const Residual8 r = res;
+      if (row + STEP < 32) fetch(row + STEP);
+      act8(v, a.act);
+      const int m = mw + row;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if constexpr (GATED) v[e] *= u[e];
+        if (a.residual && wide) v[e] += r.get(a, e);
+      }
+      if (m >= a.M || n >= a.N) continue;
+      if (wide) {
+        store8(a, m * a.ldo + n, v);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (n + e < a.N)
+            store_out(a, m * a.ldo + n + e,
+                      a.residual ? v[e] + load_out(a, a.residual, m * a.ldr + n + e) : v[e]);
+      }
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   }
