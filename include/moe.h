@@ -327,7 +327,7 @@ typedef enum {
 /* Supported: 0 <= M <= 2^24; 1 <= N, K <= 2^20; M N <= 2^40; K and the strides of x and W
  * multiples of 16 bytes (K: of 16 with 8-bit weights); x and W 16-byte aligned, the other
  * tensors to their element; strides not below the row's length (else MOE_E_SHAPE) nor above
- * 2^31. */
+ * 2^24. */
 typedef struct {
   int64_t M, N, K;
   int64_t ldx, ldw, ldr, ldo;   /* row strides of x, W (both of a gated pair), residual, out */

@@ -5,6 +5,7 @@
 // whose place a sparse layer takes (SwiGLU: the gated form with SiLU, then the plain form).
 #include <math.h>
 
+#include <algorithm>
 #include <atomic>
 #include <type_traits>
 
@@ -150,27 +151,26 @@ __global__ __launch_bounds__(kStreamThreads) void linear_rows_kernel(LinearArgs 
 }
 
 // ------------------------------------------------------------------ MFMA tiles
-// A tile of 64 MB rows by 64 NB weight rows per workgroup of 4 waves (2 x 2), a wave holding
-// MB x NB blocks of 32 x 32 sums.  K runs in steps of 128 bytes of an x row through two LDS
-// stages that global loads fill directly (no registers between).  A step is four slices of
-// one k range per MFMA block; the operands of slice s + 1 are read from LDS while the MFMAs
-// of slice s run.  The barrier that frees a stage stands before the last slice's MFMAs,
-// whose operands are in registers by then, so the other stage's first reads and the loads
-// of the step after next run under them.
+// A tile per workgroup of WM x WN waves, a wave holding MB x NB blocks of 32 x 32 sums.  K
+// runs in steps of 128 bytes of an x row through two LDS stages that global loads fill
+// directly (no registers between).  A step is four slices of one k range per MFMA block; the
+// operands of slice s + 1 are read from LDS while the MFMAs of slice s run.  The barrier that
+// frees a stage stands before the last slice's MFMAs, whose operands are in registers by
+// then, so the other stage's first reads and the loads of the step after next run under them.
 //   LDS rows are 128 bytes (8-bit weights: 64), the 16-byte chunk c of row r at position
-// c ^ (r % 8) (8-bit: c ^ (r / 2 % 4)), applied to the addresses that the lanes load from:
-// a direct load puts lane l's 16 bytes at 16 l.  The operand reads of 8 neighbouring rows
-// then take 8 different positions.
+// c ^ (r / 2 % 8) (8-bit: c ^ (r / 4 % 4)), applied to the addresses that the lanes load
+// from: a direct load puts lane l's 16 bytes at 16 l.  The operand reads of 16 neighbouring
+// rows then cover 256 bytes, all 64 banks.
 //   Gated: the weight blocks of a wave alternate gate and up rows of the same columns, so
 // act(g) * u is formed in registers.
 typedef float floatx16 __attribute__((ext_vector_type(16)));
 
-// 16 bytes per lane from g straight into LDS at lds + 16 lane (lds: byte offset, uniform).
-// The compiler does not count this load: wait with wait_loads() before the barrier after
-// which the data is read.
-__device__ __forceinline__ void load_to_lds(const void* g, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
-               :: "v"(g), "s"(lds));   // nothing else here uses m0
+// 16 bytes per lane from base + off straight into LDS at lds + 16 lane (base and lds, a byte
+// offset, are uniform).  The compiler does not count this load: wait with wait_loads()
+// before the barrier after which the data is read.
+__device__ __forceinline__ void load_to_lds(const char* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+               :: "v"(off), "s"(base), "s"(lds));   // nothing else here uses m0
 }
 // Every load to LDS has landed, every LDS read of this wave is done, LDS contents are new to
 // the compiler.
@@ -220,19 +220,26 @@ struct Tile<float> {
 
 constexpr int kXRow = 128;   // bytes of an x row in a stage
 
-template <typename WT, int MB, int NB>
+// Rows of x, weight rows and outputs of a tile.
+template <int MB, int WM>
+constexpr int tile_m() { return 32 * MB * WM; }
+template <int NB, int WN>
+constexpr int tile_w() { return 32 * NB * WN; }
+template <int NB, int WN, bool GATED>
+constexpr int tile_n() { return tile_w<NB, WN>() / (GATED ? 2 : 1); }
+template <typename WT, int MB, int NB, int WM, int WN>
 constexpr int tile_stage_bytes() {
-  return 64 * MB * kXRow + 64 * NB * Tile<WT>::WROW;
+  return tile_m<MB, WM>() * kXRow + tile_w<NB, WN>() * Tile<WT>::WROW;
 }
 // The epilogue's transpose buffer: 32 rows of a wave's sums, padded by 4 floats.
 template <int NB>
 constexpr int tile_epilogue_ld() {
   return 32 * NB + 4;
 }
-template <typename WT, int MB, int NB>
+template <typename WT, int MB, int NB, int WM, int WN>
 constexpr int tile_lds_bytes() {
-  const int stages = 2 * tile_stage_bytes<WT, MB, NB>();
-  const int epi = 4 * 32 * tile_epilogue_ld<NB>() * 4;
+  const int stages = 2 * tile_stage_bytes<WT, MB, NB, WM, WN>();
+  const int epi = WM * WN * 32 * tile_epilogue_ld<NB>() * 4;
   return stages > epi ? stages : epi;
 }
 
@@ -247,39 +254,50 @@ __device__ inline void tile_of(const LinearArgs& a, int tiles_m, int tiles_n, in
   tn = pos % per / rows;
 }
 
-template <typename WT, int MB, int NB, bool GATED>
-__global__ __launch_bounds__(256, MB * NB >= 8 ? 1 : 2) void linear_tile_kernel(LinearArgs a) {
+template <typename WT, int MB, int NB, int WM, int WN, bool GATED>
+__global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearArgs a) {
   typedef Tile<WT> TT;
   typedef typename TT::X XT;
   static_assert(!GATED || NB % 2 == 0, "gate and up blocks come in pairs");
-  constexpr int BM = 64 * MB, BN = 64 * NB, OUT_N = GATED ? BN / 2 : BN;
-  constexpr int STAGE = tile_stage_bytes<WT, MB, NB>(), XBYTES = BM * kXRow;
+  constexpr int BM = tile_m<MB, WM>(), OUT_N = tile_n<NB, WN, GATED>();
+  constexpr int STAGE = tile_stage_bytes<WT, MB, NB, WM, WN>(), XBYTES = BM * kXRow;
   constexpr bool W8 = sizeof(WT) == 1;
-  constexpr int WRPL = W8 ? 16 : 8;                    // weight rows per load
-  constexpr int NX = BM / 8 / 4, NW = BN / WRPL / 4;   // loads per wave and step
+  constexpr int WRPL = W8 ? 16 : 8;   // weight rows per load
+  // loads per wave and step
+  constexpr int NX = BM / 8 / (WM * WN), NW = tile_w<NB, WN>() / WRPL / (WM * WN);
+  static_assert(NX % 2 == 0 && (NW % 2 == 0 || (W8 && NW * WRPL <= 32)), "loads per wave");
+  static_assert(!GATED || NW * WRPL <= 64, "half of a wave's weight rows are of one matrix");
   extern __shared__ __align__(16) char smem[];
   const int tid = threadIdx.x, lane = tid & 63;
-  const int w = __builtin_amdgcn_readfirstlane(tid >> 6), wm = w >> 1, wn = w & 1;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6), wm = w / WN, wn = w % WN;
   int tm, tn;
   tile_of(a, (a.M + BM - 1) / BM, (a.N + OUT_N - 1) / OUT_N, tm, tn);
   const int m0 = tm * BM, n0 = tn * OUT_N;
 
-  // What this lane loads: rows of the tile (clamped into the matrices) at its chunk.
-  const int xchunk = (lane & 7) ^ (lane >> 3);
-  const int wchunk = W8 ? (lane & 3) ^ ((lane >> 3) & 3) : xchunk;
-  const char* px[NX];
-  const char* pw[NW];
+  // What this lane loads: rows of the tile (clamped into the matrices) at its chunk, as 32-bit
+  // offsets from the tile's first rows (the host keeps tiles within 4 GB of them).  Load i of
+  // x takes 8 rows, chunk lane % 8 ^ row / 2 % 8, whose third bit is the parity of i.
+  const uint32_t xrow = (uint32_t)(a.ldx * (int)sizeof(XT)), wrow = (uint32_t)(a.ldw * (int)sizeof(WT));
+  const int xchunk = (lane & 7) ^ (lane >> 4);
+  const int wchunk = W8 ? (lane & 3) ^ ((lane >> 4) & 3) : xchunk;
+  uint32_t ox[NX], ow[NW];
 #pragma unroll
   for (int i = 0; i < NX; ++i) {
-    const int m = min(m0 + (w * NX + i) * 8 + (lane >> 3), a.M - 1);
-    px[i] = (const char*)a.x + m * a.ldx * (int)sizeof(XT) + 16 * xchunk;
+    const int m = min(m0 + (w * NX + i) * 8 + (lane >> 3), a.M - 1) - m0;
+    ox[i] = (uint32_t)m * xrow + 16 * (xchunk ^ (4 * (i & 1)));
   }
 #pragma unroll
   for (int i = 0; i < NW; ++i) {
     const int j = (w * NW + i) * WRPL + (W8 ? lane >> 2 : lane >> 3);
-    const int mat = GATED ? (j >> 5) & 1 : 0;
     const int col = GATED ? (j / (32 * NB)) * (16 * NB) + ((j / 32) % NB >> 1) * 32 + (j & 31) : j;
-    pw[i] = (const char*)a.W[mat] + min(n0 + col, a.N - 1) * a.ldw * (int)sizeof(WT) + 16 * wchunk;
+    ow[i] = (uint32_t)(min(n0 + col, a.N - 1) - n0) * wrow + 16 * (wchunk ^ (W8 ? 0 : 4 * (i & 1)));
+  }
+  const char* bx = (const char*)a.x + (int64_t)m0 * xrow;
+  const char* bw[2];   // of each half of the wave's weight rows
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int mat = GATED ? ((w * NW + h * (NW / 2)) * WRPL >> 5) & 1 : 0;
+    bw[h] = (const char*)(mat ? a.W[1] : a.W[0]) + (int64_t)n0 * wrow;
   }
   const int nk = (a.K + TT::BK - 1) / TT::BK, nfull = a.K / TT::BK;
   // Load i of step t into its stage; a last step that K does not fill (TAIL) has zeros past K.
@@ -288,17 +306,23 @@ __global__ __launch_bounds__(256, MB * NB >= 8 ? 1 : 2) void linear_tile_kernel(
     const int q = isx ? i : i - NX;
     const uint32_t dst = (uint32_t)((t & 1) * STAGE + (isx ? (w * NX + q) * 1024
                                                            : XBYTES + (w * NW + q) * 1024));
-    const char* src = isx ? px[isx ? q : 0] : pw[isx ? 0 : q];
-    const int k = t * TT::BK + (isx ? xchunk * (16 / (int)sizeof(XT))
-                                    : wchunk * (16 / (int)sizeof(WT)));
-    if (!decltype(tail)::value || k < a.K)
-      load_to_lds(src, dst);
-    else
-      *reinterpret_cast<u32x4*>(smem + dst + 16 * lane) = u32x4{0, 0, 0, 0};
-    if (isx)
-      px[isx ? q : 0] += kXRow;
-    else
-      pw[isx ? 0 : q] += TT::WROW;
+    const char* base = isx ? bx : bw[q >= NW / 2 && NW > 1 ? 1 : 0];
+    const uint32_t off = isx ? ox[isx ? q : 0] : ow[isx ? 0 : q];
+    if constexpr (decltype(tail)::value) {
+      const int chunk = isx ? xchunk ^ (4 * (q & 1)) : wchunk ^ (W8 ? 0 : 4 * (q & 1));
+      const int k = t * TT::BK + chunk * (16 / (int)(isx ? sizeof(XT) : sizeof(WT)));
+      if (k < a.K)
+        load_to_lds(base, off, dst);
+      else
+        *reinterpret_cast<u32x4*>(smem + dst + 16 * lane) = u32x4{0, 0, 0, 0};
+    } else {
+      load_to_lds(base, off, dst);
+    }
+    if (i == NX + NW - 1) {
+      bx += kXRow;
+      bw[0] += TT::WROW;
+      bw[1] += TT::WROW;
+    }
   };
   auto load_step = [&](int t) {
     if (t < nfull) {
@@ -312,9 +336,9 @@ __global__ __launch_bounds__(256, MB * NB >= 8 ? 1 : 2) void linear_tile_kernel(
 
   // Operand reads: row lane % 32 of a block, lane half = k half of the slice.
   const int fr = lane & 31, fh = lane >> 5;
-  const int xrd = (wm * 32 * MB + fr) * kXRow, xsw = 16 * (fh ^ (fr & 7));
+  const int xrd = (wm * 32 * MB + fr) * kXRow, xsw = 16 * (fh ^ ((fr >> 1) & 7));
   const int wrd = XBYTES + (wn * 32 * NB + fr) * TT::WROW;
-  const int wsw = W8 ? 16 * ((fr >> 1) & 3) : xsw;
+  const int wsw = W8 ? 16 * ((fr >> 2) & 3) : xsw;
   u32x4 xf[2][MB];
   typename TT::WReg wf[2][NB];
   auto read_x = [&](int buf, int mb, int st, int s) {
@@ -462,22 +486,22 @@ __global__ __launch_bounds__(256, MB * NB >= 8 ? 1 : 2) void linear_tile_kernel(
 }
 
 // The LDS of a tile kernel is above the default limit: raised once per device and kernel.
-template <typename WT, int MB, int NB, bool GATED>
+template <typename WT, int MB, int NB, int WM, int WN, bool GATED>
 static hipError_t run_tiles(const LinearArgs& a, hipStream_t s) {
   static std::atomic<bool> done[kMaxDevices];
-  constexpr int lds = tile_lds_bytes<WT, MB, NB>();
+  constexpr int lds = tile_lds_bytes<WT, MB, NB, WM, WN>();
   int dev = 0;
   hipError_t e = hipGetDevice(&dev);
   if (e != hipSuccess) return e;
   if (dev < 0 || dev >= kMaxDevices || !done[dev].load(std::memory_order_acquire)) {
-    e = hipFuncSetAttribute((const void*)linear_tile_kernel<WT, MB, NB, GATED>,
+    e = hipFuncSetAttribute((const void*)linear_tile_kernel<WT, MB, NB, WM, WN, GATED>,
                             hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) return e;
     if (dev >= 0 && dev < kMaxDevices) done[dev].store(true, std::memory_order_release);
   }
-  const int64_t tiles = ceil_div(a.M, 64 * MB) * ceil_div(a.N, 64 * NB / (GATED ? 2 : 1));
-  hipLaunchKernelGGL((linear_tile_kernel<WT, MB, NB, GATED>), dim3((unsigned)tiles), dim3(256),
-                     lds, s, a);
+  const int64_t tiles = ceil_div(a.M, tile_m<MB, WM>()) * ceil_div(a.N, tile_n<NB, WN, GATED>());
+  hipLaunchKernelGGL((linear_tile_kernel<WT, MB, NB, WM, WN, GATED>), dim3((unsigned)tiles),
+                     dim3(64 * WM * WN), lds, s, a);
   return hipGetLastError();
 }
 
@@ -489,13 +513,19 @@ static hipError_t launch_linear_t(const LinearArgs& a, hipStream_t s) {
                        a);
     return hipGetLastError();
   }
-  // Largest tile that still gives every CU one; below that, what gives the most.
+  // Largest tile (x rows by weight rows) that still gives every CU one; below that, what gives
+  // the most.  Tiles taller than 64 address their rows from the first with 32 bits.
   const int64_t cus = device_cu_count(), out = GATED ? 2 : 1;
-  auto tiles = [&](int mb, int nb) { return ceil_div(a.M, 64 * mb) * ceil_div(a.N * out, 64 * nb); };
-  if (tiles(4, 4) >= cus) return run_tiles<WT, 4, 4, GATED>(a, s);
-  if (tiles(4, 2) >= cus) return run_tiles<WT, 4, 2, GATED>(a, s);
-  if (tiles(2, 2) >= cus) return run_tiles<WT, 2, 2, GATED>(a, s);
-  return run_tiles<WT, 1, GATED ? 2 : 1, GATED>(a, s);
+  const int64_t row = std::max(a.ldx * (int64_t)sizeof(typename Tile<WT>::X),
+                               a.ldw * (int64_t)sizeof(WT));
+  const bool near_rows = row * 256 < ((int64_t)1 << 32);
+  auto fills = [&](int m, int n) {
+    return near_rows && ceil_div(a.M, m) * ceil_div(a.N * out, n) >= cus;
+  };
+  if (fills(256, 256)) return run_tiles<WT, 4, 2, 2, 4, GATED>(a, s);
+  if (fills(256, 128)) return run_tiles<WT, 2, 2, 4, 2, GATED>(a, s);
+  if (fills(128, 128)) return run_tiles<WT, 2, 2, 2, 2, GATED>(a, s);
+  return run_tiles<WT, 1, GATED ? 2 : 1, 2, 2, GATED>(a, s);
 }
 
 template <typename WT>
@@ -511,7 +541,7 @@ static hipError_t launch_linear(const moe_linear_desc_t& d, const LinearArgs& a,
 }
 
 // ------------------------------------------------------------------ host checks
-constexpr int64_t kMaxStride = (int64_t)1 << 31;
+constexpr int64_t kMaxStride = (int64_t)1 << 24;   // 64 float rows stay within 32-bit offsets
 
 static moe_status_t validate_linear(const moe_linear_desc_t* d, bool fp8) {
   if (!d) return MOE_E_NULL;

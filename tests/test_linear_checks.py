@@ -46,7 +46,8 @@ def desc(**kw):
     ({"ldo": 99}, 2, 2),
     ({"ldr": 101, "ldo": 103}, 0, 0),
     ({"ldx": -8}, 2, 2),
-    ({"ldo": (1 << 31) + 1}, 3, 3),
+    ({"ldo": (1 << 24) + 1}, 3, 3),
+    ({"ldx": 1 << 24, "ldo": 1 << 24}, 0, 0),
     ({"M": (1 << 24) + 1}, 3, 3),
     ({"N": (1 << 20) + 1}, 3, 3),
     ({"K": 1 << 21}, 3, 3),
