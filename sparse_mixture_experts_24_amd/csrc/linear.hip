@@ -152,11 +152,11 @@ __global__ __launch_bounds__(kStreamThreads) void linear_rows_kernel(LinearArgs 
 
 // ------------------------------------------------------------------ MFMA tiles
 // A tile per workgroup of WM x WN waves, a wave holding MB x NB blocks of 32 x 32 sums.  K
-// runs in steps of 128 bytes of an x row through two LDS stages that global loads fill
+// runs in steps of 128 bytes of an x row through ST LDS stages that global loads fill
 // directly (no registers between).  A step is four slices of one k range per MFMA block; the
 // operands of slice s + 1 are read from LDS while the MFMAs of slice s run.  The barrier that
 // frees a stage stands before the last slice's MFMAs, whose operands are in registers by
-// then, so the other stage's first reads and the loads of the step after next run under them.
+// then, so the next stage's first reads and the loads ST steps ahead run under them.
 //   LDS rows are 128 bytes (8-bit weights: 64), the 16-byte chunk c of row r at position
 // c ^ (r / 2 % 8) (8-bit: c ^ (r / 4 % 4)), applied to the addresses that the lanes load
 // from: a direct load puts lane l's 16 bytes at 16 l.  The operand reads of 16 neighbouring
@@ -172,10 +172,11 @@ __device__ __forceinline__ void load_to_lds(const char* base, uint32_t off, uint
   asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
                :: "v"(off), "s"(base), "s"(lds));   // nothing else here uses m0
 }
-// Every load to LDS has landed, every LDS read of this wave is done, LDS contents are new to
-// the compiler.
+// All but the youngest N of the wave's loads to LDS have landed, every LDS read of this wave is
+// done, LDS contents are new to the compiler.
+template <int N = 0>
 __device__ __forceinline__ void wait_loads() {
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
 }
 // Barrier that LDS accesses do not cross.
 __device__ __forceinline__ void stage_barrier() {
@@ -236,9 +237,9 @@ template <int NB>
 constexpr int tile_epilogue_ld() {
   return 32 * NB + 4;
 }
-template <typename WT, int MB, int NB, int WM, int WN>
+template <typename WT, int MB, int NB, int WM, int WN, int ST>
 constexpr int tile_lds_bytes() {
-  const int stages = 2 * tile_stage_bytes<WT, MB, NB, WM, WN>();
+  const int stages = ST * tile_stage_bytes<WT, MB, NB, WM, WN>();
   const int epi = WM * WN * 32 * tile_epilogue_ld<NB>() * 4;
   return stages > epi ? stages : epi;
 }
@@ -254,7 +255,7 @@ __device__ inline void tile_of(const LinearArgs& a, int tiles_m, int tiles_n, in
   tn = pos % per / rows;
 }
 
-template <typename WT, int MB, int NB, int WM, int WN, bool GATED>
+template <typename WT, int MB, int NB, int WM, int WN, int ST, bool GATED>
 __global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearArgs a) {
   typedef Tile<WT> TT;
   typedef typename TT::X XT;
@@ -300,12 +301,13 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearArgs a)
     bw[h] = (const char*)(mat ? a.W[1] : a.W[0]) + (int64_t)n0 * wrow;
   }
   const int nk = (a.K + TT::BK - 1) / TT::BK, nfull = a.K / TT::BK;
-  // Load i of step t into its stage; a last step that K does not fill (TAIL) has zeros past K.
-  auto load = [&](auto tail, int i, int t) {
+  // Load i of step t into the stage at `stage`; a last step that K does not fill (tail) has
+  // zeros past K.
+  auto load = [&](auto tail, int i, int t, int stage) {
     const bool isx = i < NX;
     const int q = isx ? i : i - NX;
-    const uint32_t dst = (uint32_t)((t & 1) * STAGE + (isx ? (w * NX + q) * 1024
-                                                           : XBYTES + (w * NW + q) * 1024));
+    const uint32_t dst = (uint32_t)(stage + (isx ? (w * NX + q) * 1024
+                                                    : XBYTES + (w * NW + q) * 1024));
     const char* base = isx ? bx : bw[q >= NW / 2 && NW > 1 ? 1 : 0];
     const uint32_t off = isx ? ox[isx ? q : 0] : ow[isx ? 0 : q];
     if constexpr (decltype(tail)::value) {
@@ -324,13 +326,13 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearArgs a)
       bw[1] += TT::WROW;
     }
   };
-  auto load_step = [&](int t) {
+  auto load_step = [&](int t, int stage) {
     if (t < nfull) {
 #pragma unroll
-      for (int i = 0; i < NX + NW; ++i) load(std::false_type{}, i, t);
+      for (int i = 0; i < NX + NW; ++i) load(std::false_type{}, i, t, stage);
     } else if (t < nk) {
 #pragma unroll
-      for (int i = 0; i < NX + NW; ++i) load(std::true_type{}, i, t);
+      for (int i = 0; i < NX + NW; ++i) load(std::true_type{}, i, t, stage);
     }
   };
 
@@ -342,12 +344,12 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearArgs a)
   u32x4 xf[2][MB];
   typename TT::WReg wf[2][NB];
   auto read_x = [&](int buf, int mb, int st, int s) {
-    xf[buf][mb] = *reinterpret_cast<const u32x4*>(smem + st * STAGE + xrd + mb * 32 * kXRow +
+    xf[buf][mb] = *reinterpret_cast<const u32x4*>(smem + st + xrd + mb * 32 * kXRow +
                                                   (xsw ^ (32 * s)));
   };
   auto read_w = [&](int buf, int nb, int st, int s) {
     wf[buf][nb] = *reinterpret_cast<const typename TT::WReg*>(
-        smem + st * STAGE + wrd + nb * 32 * TT::WROW + (W8 ? (wsw ^ (16 * s)) + 8 * fh
+        smem + st + wrd + nb * 32 * TT::WROW + (W8 ? (wsw ^ (16 * s)) + 8 * fh
                                                            : wsw ^ (32 * s)));
   };
   floatx16 acc[MB][NB];
@@ -358,32 +360,41 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearArgs a)
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
 
-  load_step(0);
-  wait_loads();
+  constexpr int L = NX + NW;
+#pragma unroll
+  for (int t = 0; t < ST; ++t) load_step(t, t * STAGE);
+  if (ST <= nfull)
+    wait_loads<(ST - 1) * L>();
+  else
+    wait_loads();
   stage_barrier();
-  load_step(1);
 #pragma unroll
   for (int i = 0; i < MB; ++i) read_x(0, i, 0, 0);
 #pragma unroll
   for (int i = 0; i < NB; ++i) read_w(0, i, 0, 0);
-  // Step t.  BODY: step t + 2 is a full one, whose loads go out between the last slice's MFMAs,
-  // as early as its stage is free.
+  // Step t.  Body: step t + ST is a full one, whose loads go out between the last slice's
+  // MFMAs, as early as its stage is free.
+  int stage = 0;
   auto step = [&](auto body, int t) {
+    const int now = stage, next = ST == 2 ? STAGE - now : now == (ST - 1) * STAGE ? 0 : now + STAGE;
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
-      const int buf = s & 1, st = s < 3 ? t & 1 : (t + 1) & 1, sn = (s + 1) & 3;
+      const int buf = s & 1, st = s < 3 ? now : next, sn = (s + 1) & 3;
       if (s == 3) {
-        // stage t is read out by every wave, stage t + 1 has landed
-        wait_loads();
+        // step t's stage is read out by every wave, step t + 1 has landed
+        if constexpr (decltype(body)::value)
+          wait_loads<(ST - 2) * L>();
+        else
+          wait_loads();
         stage_barrier();
-        if constexpr (!decltype(body)::value) load_step(t + 2);
+        if constexpr (!decltype(body)::value) load_step(t + ST, now);
       }
       u32x4 wo[NB];
 #pragma unroll
       for (int i = 0; i < NB; ++i) wo[i] = TT::operand(wf[buf][i]);
       // One operand read of the next slice (past the last step: stale, unused) after each
       // MFMA, in whose shadow it issues.
-      constexpr int B = MB * NB, RD = MB + NB, L = NX + NW, kPerMma = (RD + B - 1) / B;
+      constexpr int B = MB * NB, RD = MB + NB, kPerMma = (RD + B - 1) / B;
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int i = 0; i < MB; ++i)
@@ -401,16 +412,17 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearArgs a)
           if constexpr (decltype(body)::value) {
             if (s == 3) {
 #pragma unroll
-              for (int l = q * L / B; l < (q + 1) * L / B; ++l) load(std::false_type{}, l, t + 2);
+              for (int l = q * L / B; l < (q + 1) * L / B; ++l) load(std::false_type{}, l, t + ST, now);
             }
           }
           __builtin_amdgcn_sched_barrier(0);
         }
       __builtin_amdgcn_sched_barrier(0);
     }
+    stage = next;
   };
   int t = 0;
-  for (; t + 2 < nfull; ++t) step(std::true_type{}, t);
+  for (; t + ST < nfull; ++t) step(std::true_type{}, t);
   for (; t < nk; ++t) step(std::false_type{}, t);
   wait_loads();
   stage_barrier();   // the stages are free for the transposes
@@ -486,21 +498,21 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearArgs a)
 }
 
 // The LDS of a tile kernel is above the default limit: raised once per device and kernel.
-template <typename WT, int MB, int NB, int WM, int WN, bool GATED>
+template <typename WT, int MB, int NB, int WM, int WN, int ST, bool GATED>
 static hipError_t run_tiles(const LinearArgs& a, hipStream_t s) {
   static std::atomic<bool> done[kMaxDevices];
-  constexpr int lds = tile_lds_bytes<WT, MB, NB, WM, WN>();
+  constexpr int lds = tile_lds_bytes<WT, MB, NB, WM, WN, ST>();
   int dev = 0;
   hipError_t e = hipGetDevice(&dev);
   if (e != hipSuccess) return e;
   if (dev < 0 || dev >= kMaxDevices || !done[dev].load(std::memory_order_acquire)) {
-    e = hipFuncSetAttribute((const void*)linear_tile_kernel<WT, MB, NB, WM, WN, GATED>,
+    e = hipFuncSetAttribute((const void*)linear_tile_kernel<WT, MB, NB, WM, WN, ST, GATED>,
                             hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) return e;
     if (dev >= 0 && dev < kMaxDevices) done[dev].store(true, std::memory_order_release);
   }
   const int64_t tiles = ceil_div(a.M, tile_m<MB, WM>()) * ceil_div(a.N, tile_n<NB, WN, GATED>());
-  hipLaunchKernelGGL((linear_tile_kernel<WT, MB, NB, WM, WN, GATED>), dim3((unsigned)tiles),
+  hipLaunchKernelGGL((linear_tile_kernel<WT, MB, NB, WM, WN, ST, GATED>), dim3((unsigned)tiles),
                      dim3(64 * WM * WN), lds, s, a);
   return hipGetLastError();
 }
@@ -522,10 +534,10 @@ static hipError_t launch_linear_t(const LinearArgs& a, hipStream_t s) {
   auto fills = [&](int m, int n) {
     return near_rows && ceil_div(a.M, m) * ceil_div(a.N * out, n) >= cus;
   };
-  if (fills(256, 256)) return run_tiles<WT, 4, 2, 2, 4, GATED>(a, s);
-  if (fills(256, 128)) return run_tiles<WT, 2, 2, 4, 2, GATED>(a, s);
-  if (fills(128, 128)) return run_tiles<WT, 2, 2, 2, 2, GATED>(a, s);
-  return run_tiles<WT, 1, GATED ? 2 : 1, 2, 2, GATED>(a, s);
+  if (fills(256, 256)) return run_tiles<WT, 4, 2, 2, 4, 2, GATED>(a, s);
+  if (fills(256, 128)) return run_tiles<WT, 2, 2, 4, 2, 3, GATED>(a, s);
+  if (fills(128, 128)) return run_tiles<WT, 2, 2, 2, 2, 2, GATED>(a, s);
+  return run_tiles<WT, 1, GATED ? 2 : 1, 2, 2, GATED ? 3 : 4, GATED>(a, s);
 }
 
 template <typename WT>
