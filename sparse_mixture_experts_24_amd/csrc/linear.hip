@@ -157,6 +157,9 @@ __global__ __launch_bounds__(kStreamThreads) void linear_rows_kernel(LinearArgs 
 // operands of slice s + 1 are read from LDS while the MFMAs of slice s run.  The barrier that
 // frees a stage stands before the last slice's MFMAs, whose operands are in registers by
 // then, so the next stage's first reads and the loads ST steps ahead run under them.
+//   Two stages whose x and weight parts are alike are five slots of one part, taken in the
+// order x, w, x, w, ...: the fifth lets the x part of step t + 2 load during step t, so only
+// its weight part waits for the barrier, and the loads spread over the whole step.
 //   LDS rows are 128 bytes (8-bit weights: 64), the 16-byte chunk c of row r at position
 // c ^ (r / 2 % 8) (8-bit: c ^ (r / 4 % 4)), applied to the addresses that the lanes load
 // from: a direct load puts lane l's 16 bytes at 16 l.  The operand reads of 16 neighbouring
@@ -237,9 +240,15 @@ template <int NB>
 constexpr int tile_epilogue_ld() {
   return 32 * NB + 4;
 }
+// Two stages of equal x and weight parts share five slots of one part instead.
+template <typename WT, int MB, int NB, int WM, int WN, int ST>
+constexpr bool tile_slots() {
+  return ST == 2 && 2 * tile_m<MB, WM>() * kXRow == tile_stage_bytes<WT, MB, NB, WM, WN>();
+}
 template <typename WT, int MB, int NB, int WM, int WN, int ST>
 constexpr int tile_lds_bytes() {
-  const int stages = ST * tile_stage_bytes<WT, MB, NB, WM, WN>();
+  const int stage = tile_stage_bytes<WT, MB, NB, WM, WN>();
+  const int stages = tile_slots<WT, MB, NB, WM, WN, ST>() ? 5 * stage / 2 : ST * stage;
   const int epi = WM * WN * 32 * tile_epilogue_ld<NB>() * 4;
   return stages > epi ? stages : epi;
 }
@@ -262,7 +271,7 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearArgs a)
   static_assert(!GATED || NB % 2 == 0, "gate and up blocks come in pairs");
   constexpr int BM = tile_m<MB, WM>(), OUT_N = tile_n<NB, WN, GATED>();
   constexpr int STAGE = tile_stage_bytes<WT, MB, NB, WM, WN>(), XBYTES = BM * kXRow;
-  constexpr bool W8 = sizeof(WT) == 1;
+  constexpr bool W8 = sizeof(WT) == 1, SLOTS = tile_slots<WT, MB, NB, WM, WN, ST>();
   constexpr int WRPL = W8 ? 16 : 8;   // weight rows per load
   // loads per wave and step
   constexpr int NX = BM / 8 / (WM * WN), NW = tile_w<NB, WN>() / WRPL / (WM * WN);
@@ -301,13 +310,12 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearArgs a)
     bw[h] = (const char*)(mat ? a.W[1] : a.W[0]) + (int64_t)n0 * wrow;
   }
   const int nk = (a.K + TT::BK - 1) / TT::BK, nfull = a.K / TT::BK;
-  // Load i of step t into the stage at `stage`; a last step that K does not fill (tail) has
-  // zeros past K.
-  auto load = [&](auto tail, int i, int t, int stage) {
+  // Load i (x part, then weight part) of step t into the part at LDS byte `part`; a last step
+  // that K does not fill (tail) has zeros past K.
+  auto load = [&](auto tail, int i, int t, int part) {
     const bool isx = i < NX;
     const int q = isx ? i : i - NX;
-    const uint32_t dst = (uint32_t)(stage + (isx ? (w * NX + q) * 1024
-                                                    : XBYTES + (w * NW + q) * 1024));
+    const uint32_t dst = (uint32_t)(part + (w * (isx ? NX : NW) + q) * 1024);
     const char* base = isx ? bx : bw[q >= NW / 2 && NW > 1 ? 1 : 0];
     const uint32_t off = isx ? ox[isx ? q : 0] : ow[isx ? 0 : q];
     if constexpr (decltype(tail)::value) {
@@ -320,26 +328,28 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearArgs a)
     } else {
       load_to_lds(base, off, dst);
     }
+    if (i == NX - 1) bx += kXRow;
     if (i == NX + NW - 1) {
-      bx += kXRow;
       bw[0] += TT::WROW;
       bw[1] += TT::WROW;
     }
   };
-  auto load_step = [&](int t, int stage) {
+  auto load_part = [&](int from, int to, int t, int part) {
     if (t < nfull) {
 #pragma unroll
-      for (int i = 0; i < NX + NW; ++i) load(std::false_type{}, i, t, stage);
+      for (int i = 0; i < NX + NW; ++i)
+        if (i >= from && i < to) load(std::false_type{}, i, t, part);
     } else if (t < nk) {
 #pragma unroll
-      for (int i = 0; i < NX + NW; ++i) load(std::true_type{}, i, t, stage);
+      for (int i = 0; i < NX + NW; ++i)
+        if (i >= from && i < to) load(std::true_type{}, i, t, part);
     }
   };
 
   // Operand reads: row lane % 32 of a block, lane half = k half of the slice.
   const int fr = lane & 31, fh = lane >> 5;
   const int xrd = (wm * 32 * MB + fr) * kXRow, xsw = 16 * (fh ^ ((fr >> 1) & 7));
-  const int wrd = XBYTES + (wn * 32 * NB + fr) * TT::WROW;
+  const int wrd = (wn * 32 * NB + fr) * TT::WROW;
   const int wsw = W8 ? 16 * ((fr >> 2) & 3) : xsw;
   u32x4 xf[2][MB];
   typename TT::WReg wf[2][NB];
@@ -362,7 +372,10 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearArgs a)
 
   constexpr int L = NX + NW;
 #pragma unroll
-  for (int t = 0; t < ST; ++t) load_step(t, t * STAGE);
+  for (int t = 0; t < ST; ++t) {
+    load_part(0, NX, t, t * STAGE);
+    load_part(NX, L, t, t * STAGE + XBYTES);
+  }
   if (ST <= nfull)
     wait_loads<(ST - 1) * L>();
   else
@@ -371,23 +384,38 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearArgs a)
 #pragma unroll
   for (int i = 0; i < MB; ++i) read_x(0, i, 0, 0);
 #pragma unroll
-  for (int i = 0; i < NB; ++i) read_w(0, i, 0, 0);
-  // Step t.  Body: step t + ST is a full one, whose loads go out between the last slice's
-  // MFMAs, as early as its stage is free.
-  int stage = 0;
+  for (int i = 0; i < NB; ++i) read_w(0, i, XBYTES, 0);
+  // Step t.  Body: step t + ST is a full one, whose loads go out between MFMAs, as early as
+  // their part is free.  px, pw: where step t's parts are.
+  int px = 0, pw = XBYTES;
+  auto part_after = [&](int part, int by) {   // the part `by` slots on
+    const int p = part + by * XBYTES;
+    return p >= 5 * XBYTES ? p - 5 * XBYTES : p;
+  };
   auto step = [&](auto body, int t) {
-    const int now = stage, next = ST == 2 ? STAGE - now : now == (ST - 1) * STAGE ? 0 : now + STAGE;
+    int nx, nw;
+    if constexpr (SLOTS) {
+      nx = part_after(px, 2);
+      nw = part_after(pw, 2);
+    } else {
+      nx = px == (ST - 1) * STAGE ? 0 : px + STAGE;
+      nw = nx + XBYTES;
+    }
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
-      const int buf = s & 1, st = s < 3 ? now : next, sn = (s + 1) & 3;
+      const int buf = s & 1, sx = s < 3 ? px : nx, sw = s < 3 ? pw : nw, sn = (s + 1) & 3;
+      if (SLOTS && s == 0 && !decltype(body)::value) load_part(0, NX, t + 2, part_after(nx, 2));
       if (s == 3) {
-        // step t's stage is read out by every wave, step t + 1 has landed
+        // step t's parts are read out by every wave, step t + 1 has landed
         if constexpr (decltype(body)::value)
-          wait_loads<(ST - 2) * L>();
+          wait_loads<SLOTS ? NX : (ST - 2) * L>();
         else
           wait_loads();
         stage_barrier();
-        if constexpr (!decltype(body)::value) load_step(t + ST, now);
+        if constexpr (!decltype(body)::value) {
+          if (!SLOTS) load_part(0, NX, t + ST, px);
+          load_part(NX, L, t + ST, SLOTS ? px : pw);
+        }
       }
       u32x4 wo[NB];
 #pragma unroll
@@ -405,21 +433,34 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearArgs a)
 #pragma unroll
           for (int l = q * kPerMma; l < (q + 1 == B ? RD : min((q + 1) * kPerMma, RD)); ++l) {
             if (l < NB)
-              read_w(buf ^ 1, l < NB ? l : 0, st, sn);
+              read_w(buf ^ 1, l < NB ? l : 0, sw, sn);
             else
-              read_x(buf ^ 1, l >= NB ? l - NB : 0, st, sn);
+              read_x(buf ^ 1, l >= NB ? l - NB : 0, sx, sn);
           }
           if constexpr (decltype(body)::value) {
-            if (s == 3) {
+            if constexpr (SLOTS) {
+              if (s < 3) {   // x part of step t + 2 over three slices
+                const int p = s * B + q;
 #pragma unroll
-              for (int l = q * L / B; l < (q + 1) * L / B; ++l) load(std::false_type{}, l, t + ST, now);
+                for (int l = p * NX / (3 * B); l < (p + 1) * NX / (3 * B); ++l)
+                  load(std::false_type{}, l, t + 2, part_after(nx, 2));
+              } else {
+#pragma unroll
+                for (int l = q * NW / B; l < (q + 1) * NW / B; ++l)
+                  load(std::false_type{}, NX + l, t + 2, px);
+              }
+            } else if (s == 3) {
+#pragma unroll
+              for (int l = q * L / B; l < (q + 1) * L / B; ++l)
+                load(std::false_type{}, l, t + ST, l < NX ? px : pw);
             }
           }
           __builtin_amdgcn_sched_barrier(0);
         }
       __builtin_amdgcn_sched_barrier(0);
     }
-    stage = next;
+    px = nx;
+    pw = nw;
   };
   int t = 0;
   for (; t + ST < nfull; ++t) step(std::true_type{}, t);
