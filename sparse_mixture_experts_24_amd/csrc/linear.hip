@@ -151,9 +151,10 @@ __global__ __launch_bounds__(kStreamThreads) void linear_rows_kernel(LinearArgs 
 }
 
 // ------------------------------------------------------------------ MFMA tiles
-// A tile per workgroup of WM x WN waves, a wave holding MB x NB blocks of 32 x 32 sums.  K
-// runs in steps of 128 bytes of an x row through ST LDS stages that global loads fill
-// directly (no registers between).  A step is four slices of one k range per MFMA block; the
+// A tile per workgroup of WM x WN waves, a wave holding MB x NB blocks of 32 x 32 sums (each
+// four MFMAs of 16 x 16: the 32 x 32 MFMA moves twice the sums through the registers per
+// product, and large products run at the clock that the card's power allows).  K runs in steps of 128 bytes of an x row through ST LDS stages that global loads fill
+// directly (no registers between).  A step is two slices of one k range per MFMA block; the
 // operands of slice s + 1 are read from LDS while the MFMAs of slice s run.  The barrier that
 // frees a stage stands before the last slice's MFMAs, whose operands are in registers by
 // then, so the next stage's first reads and the loads ST steps ahead run under them.
@@ -166,8 +167,6 @@ __global__ __launch_bounds__(kStreamThreads) void linear_rows_kernel(LinearArgs 
 // rows then cover 256 bytes, all 64 banks.
 //   Gated: the weight blocks of a wave alternate gate and up rows of the same columns, so
 // act(g) * u is formed in registers.
-typedef float floatx16 __attribute__((ext_vector_type(16)));
-
 // 16 bytes per lane from base + off straight into LDS at lds + 16 lane (base and lds, a byte
 // offset, are uniform).  The compiler does not count this load: wait with wait_loads()
 // before the barrier after which the data is read.
@@ -187,13 +186,15 @@ __device__ __forceinline__ void stage_barrier() {
   asm volatile("" ::: "memory");
 }
 
+// One MFMA block's product of a slice: 64 bytes of the x rows.  Lane (row, group g) holds the
+// 16-byte chunk g of its x row's slice, and the weights of the same k.
 template <typename WT>
 struct Tile {   // bf16
   static constexpr int BK = 64, WROW = 128;   // k per step, bytes of a weight row in it
   typedef bf16_t X;
   typedef u32x4 WReg;
-  __device__ static void mma(floatx16& acc, u32x4 x, u32x4 w) {
-    acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, x),
+  __device__ static void mma(floatx4& acc, u32x4 x, u32x4 w) {
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x),
                                                   __builtin_bit_cast(bf16x8, w), acc, 0, 0, 0);
   }
   __device__ static u32x4 operand(u32x4 w) { return w; }
@@ -203,7 +204,7 @@ struct Tile<uint8_t> {
   static constexpr int BK = 64, WROW = 64;
   typedef bf16_t X;
   typedef uint2 WReg;
-  __device__ static void mma(floatx16& acc, u32x4 x, u32x4 w) { Tile<bf16_t>::mma(acc, x, w); }
+  __device__ static void mma(floatx4& acc, u32x4 x, u32x4 w) { Tile<bf16_t>::mma(acc, x, w); }
   __device__ static u32x4 operand(uint2 w) {
     return __builtin_bit_cast(u32x4, widen_e4m3(w.x, w.y));
   }
@@ -213,10 +214,10 @@ struct Tile<float> {
   static constexpr int BK = 32, WROW = 128;
   typedef float X;
   typedef u32x4 WReg;
-  __device__ static void mma(floatx16& acc, u32x4 x, u32x4 w) {
+  __device__ static void mma(floatx4& acc, u32x4 x, u32x4 w) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)   // lane half h holds k = 4 h + j
-      acc = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(x[j]), __uint_as_float(w[j]), acc,
+    for (int j = 0; j < 4; ++j)   // group g holds k = 4 g + j
+      acc = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(x[j]), __uint_as_float(w[j]), acc,
                                                  0, 0, 0);
   }
   __device__ static u32x4 operand(u32x4 w) { return w; }
@@ -346,29 +347,26 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearArgs a)
     }
   };
 
-  // Operand reads: row lane % 32 of a block, lane half = k half of the slice.
-  const int fr = lane & 31, fh = lane >> 5;
-  const int xrd = (wm * 32 * MB + fr) * kXRow, xsw = 16 * (fh ^ ((fr >> 1) & 7));
+  // Operand reads: row lane % 16 of a 16-row block, chunk lane / 16 of the slice.
+  constexpr int XB = 2 * MB, WB = 2 * NB;
+  const int fr = lane & 15, fg = lane >> 4;
+  const int xrd = (wm * 32 * MB + fr) * kXRow, xsw = 16 * (fg ^ ((fr >> 1) & 7));
   const int wrd = (wn * 32 * NB + fr) * TT::WROW;
-  const int wsw = W8 ? 16 * ((fr >> 2) & 3) : xsw;
-  u32x4 xf[2][MB];
-  typename TT::WReg wf[2][NB];
-  auto read_x = [&](int buf, int mb, int st, int s) {
-    xf[buf][mb] = *reinterpret_cast<const u32x4*>(smem + st + xrd + mb * 32 * kXRow +
-                                                  (xsw ^ (32 * s)));
+  const int wsw = W8 ? 16 * ((fg >> 1) ^ ((fr >> 2) & 3)) : xsw;
+  u32x4 xf[2][XB];
+  typename TT::WReg wf[2][WB];
+  auto read_x = [&](int buf, int i, int part, int s) {
+    xf[buf][i] = *reinterpret_cast<const u32x4*>(smem + part + xrd + i * 16 * kXRow + (xsw ^ (64 * s)));
   };
-  auto read_w = [&](int buf, int nb, int st, int s) {
-    wf[buf][nb] = *reinterpret_cast<const typename TT::WReg*>(
-        smem + st + wrd + nb * 32 * TT::WROW + (W8 ? (wsw ^ (16 * s)) + 8 * fh
-                                                           : wsw ^ (32 * s)));
+  auto read_w = [&](int buf, int i, int part, int s) {
+    wf[buf][i] = *reinterpret_cast<const typename TT::WReg*>(
+        smem + part + wrd + i * 16 * TT::WROW + (W8 ? (wsw ^ (32 * s)) + 8 * (fg & 1) : wsw ^ (64 * s)));
   };
-  floatx16 acc[MB][NB];
+  floatx4 acc[XB][WB];
 #pragma unroll
-  for (int i = 0; i < MB; ++i)
+  for (int i = 0; i < XB; ++i)
 #pragma unroll
-    for (int j = 0; j < NB; ++j)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+    for (int j = 0; j < WB; ++j) acc[i][j] = floatx4{0.f, 0.f, 0.f, 0.f};
 
   constexpr int L = NX + NW;
 #pragma unroll
@@ -382,9 +380,9 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearArgs a)
     wait_loads();
   stage_barrier();
 #pragma unroll
-  for (int i = 0; i < MB; ++i) read_x(0, i, 0, 0);
+  for (int i = 0; i < XB; ++i) read_x(0, i, 0, 0);
 #pragma unroll
-  for (int i = 0; i < NB; ++i) read_w(0, i, XBYTES, 0);
+  for (int i = 0; i < WB; ++i) read_w(0, i, XBYTES, 0);
   // Step t.  Body: step t + ST is a full one, whose loads go out between MFMAs, as early as
   // their part is free.  px, pw: where step t's parts are.
   int px = 0, pw = XBYTES;
@@ -402,10 +400,10 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearArgs a)
       nw = nx + XBYTES;
     }
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      const int buf = s & 1, sx = s < 3 ? px : nx, sw = s < 3 ? pw : nw, sn = (s + 1) & 3;
+    for (int s = 0; s < 2; ++s) {
+      const int buf = s, sx = s == 0 ? px : nx, sw = s == 0 ? pw : nw, sn = s ^ 1;
       if (SLOTS && s == 0 && !decltype(body)::value) load_part(0, NX, t + 2, part_after(nx, 2));
-      if (s == 3) {
+      if (s == 1) {
         // step t's parts are read out by every wave, step t + 1 has landed
         if constexpr (decltype(body)::value)
           wait_loads<SLOTS ? NX : (ST - 2) * L>();
@@ -417,39 +415,38 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearArgs a)
           load_part(NX, L, t + ST, SLOTS ? px : pw);
         }
       }
-      u32x4 wo[NB];
+      u32x4 wo[WB];
 #pragma unroll
-      for (int i = 0; i < NB; ++i) wo[i] = TT::operand(wf[buf][i]);
-      // One operand read of the next slice (past the last step: stale, unused) after each
-      // MFMA, in whose shadow it issues.
-      constexpr int B = MB * NB, RD = MB + NB, kPerMma = (RD + B - 1) / B;
+      for (int i = 0; i < WB; ++i) wo[i] = TT::operand(wf[buf][i]);
+      // Operand reads of the next slice (past the last step: stale, unused) go out one by one
+      // between the MFMAs, in whose shadow they issue.
+      constexpr int B = XB * WB, RD = XB + WB, EVERY = B >= 2 * RD ? 2 : 1;
+      static_assert(RD <= B, "a read per MFMA at most");
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int i = 0; i < MB; ++i)
+      for (int i = 0; i < XB; ++i)
 #pragma unroll
-        for (int j = 0; j < NB; ++j) {
-          const int q = i * NB + j;
+        for (int j = 0; j < WB; ++j) {
+          const int q = i * WB + j, rd = q / EVERY;
           TT::mma(acc[i][j], xf[buf][i], wo[j]);
-#pragma unroll
-          for (int l = q * kPerMma; l < (q + 1 == B ? RD : min((q + 1) * kPerMma, RD)); ++l) {
-            if (l < NB)
-              read_w(buf ^ 1, l < NB ? l : 0, sw, sn);
+          if (q % EVERY == 0 && rd < RD) {
+            if (rd < WB)
+              read_w(buf ^ 1, rd < WB ? rd : 0, sw, sn);
             else
-              read_x(buf ^ 1, l >= NB ? l - NB : 0, sx, sn);
+              read_x(buf ^ 1, rd >= WB ? rd - WB : 0, sx, sn);
           }
           if constexpr (decltype(body)::value) {
             if constexpr (SLOTS) {
-              if (s < 3) {   // x part of step t + 2 over three slices
-                const int p = s * B + q;
+              if (s == 0) {   // x part of step t + 2
 #pragma unroll
-                for (int l = p * NX / (3 * B); l < (p + 1) * NX / (3 * B); ++l)
+                for (int l = q * NX / B; l < (q + 1) * NX / B; ++l)
                   load(std::false_type{}, l, t + 2, part_after(nx, 2));
               } else {
 #pragma unroll
                 for (int l = q * NW / B; l < (q + 1) * NW / B; ++l)
                   load(std::false_type{}, NX + l, t + 2, px);
               }
-            } else if (s == 3) {
+            } else if (s == 1) {
 #pragma unroll
               for (int l = q * L / B; l < (q + 1) * L / B; ++l)
                 load(std::false_type{}, l, t + ST, l < NX ? px : pw);
@@ -488,10 +485,12 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearArgs a)
     for (int q = 0; q < MB; ++q)
       if (q == i) {
 #pragma unroll
-        for (int j = 0; j < NB; ++j)
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int r = 0; r < 16; ++r)
-            tr[(8 * (r >> 2) + 4 * fh + (r & 3)) * LD + 32 * j + fr] = acc[q][j][r];
+          for (int j = 0; j < WB; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              tr[(16 * h + 4 * fg + r) * LD + 16 * j + fr] = acc[2 * q + h][j][r];
       }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     const int mw = m0 + (wm * MB + i) * 32 + row0;
