@@ -207,43 +207,15 @@ __global__ __launch_bounds__(kFewThreads) void few_logits_kernel(FewArgs a) {
   if (m < a.T && e0 + n < a.E) a.logits[m * a.E + e0 + n] = red_get(red, kRedWave, m, n);
 }
 
-// A workgroup's run of consecutive units of n, as even as they go.
-__device__ inline void share_of(int64_t n, int64_t& i0, int64_t& i1) {
-  i0 = n * blockIdx.x / gridDim.x;
-  i1 = n * (blockIdx.x + 1) / gridDim.x;
-}
-
-// Units of NG x 16 weight rows; NS steps of every row per wave and visit.  A ring of R steps
-// (R divides NS) runs across the visits: as step s is used, step s + R goes out, of this
-// visit or of the next, so a wave always has R NG 2 KB in flight.
-template <typename WT, int R, int NG>
-struct Ring {
-  u32x4 w[R][NG][2];
-  // base[g][i]: the lane's row of load i of group g; st0: first step, nst: steps of the row
-  __device__ __forceinline__ void load(int s, const char* const (&base)[NG][2], int st0, int nst,
-                                       int row_bytes) {
-    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-    const int st = min(st0 + s * kFewWaves + wv, nst - 1);
-    const int byte = min(st * kStepBytes + 16 * (lane & 7), row_bytes - 16);
-#pragma unroll
-    for (int g = 0; g < NG; ++g)
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        w[s % R][g][i] = *reinterpret_cast<const u32x4*>(base[g][i] + byte);
-  }
-};
-
 // h = SiLU(x W_gate^T) * (x W_up^T).  A unit is NG x (8 gate rows and the 8 matching up
 // rows) of a touched expert; all T tokens run through it (the matrix cores have the room),
-// and the rows of the tokens that chose the expert are kept.  The token operand of the
-// wave's part of d stays in registers over all units when d fits NS steps per wave.
+// and the rows of the tokens that chose the expert are kept.
 template <typename WT, int NS, int R, int NG>
 __global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(FewArgs a) {
   typedef Stream<WT> S;
   typedef typename S::X XT;
   __shared__ FewRoute r;
-  __shared__ __align__(16) char stage[kFewWaves][kStageBytes];
-  __shared__ float red[2][kFewWaves * NG * kRedWave];
+  __shared__ StreamLds<NG> lds;
   few_route(a, r);
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
   if (blockIdx.x == 0)
@@ -252,98 +224,51 @@ __global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(FewArgs a) {
   const int upe = a.F / (8 * NG);   // units per expert
   int64_t i0, i1;
   share_of((int64_t)r.nu * upe, i0, i1);
-  if (i0 == i1) return;
   const int nst = (a.d + S::SK - 1) / S::SK, row_bytes = a.d * (int)sizeof(WT);
   const int nchunk = (nst + NS * kFewWaves - 1) / (NS * kFewWaves);
-  const int t = lane & 15, g4 = lane >> 4;
-  u32x4 xs[NS][S::XR];
-  auto load_x = [&](int c) {
+  stream_units<WT, NS, R, NG, 1>(
+      i0, i1, nchunk, nst, row_bytes, lds,
+      [&](int64_t i, const char* (&base)[NG][2]) {
+        const int u = (int)(i / upe);
+        const int64_t f0 = (int64_t)r.expert[u] * a.F + (i % upe) * (8 * NG) + (lane >> 3);
 #pragma unroll
-    for (int s = 0; s < NS; ++s)
-#pragma unroll
-      for (int i = 0; i < S::XR; ++i) {
-        const int k = ((c * NS + s) * kFewWaves + wv) * S::SK + S::k_of(g4, i);
-        xs[s][i] = u32x4{0, 0, 0, 0};
-        if (t < a.T && k < a.d)
-          xs[s][i] = *reinterpret_cast<const u32x4*>((const XT*)a.x + (int64_t)t * a.d + k);
-      }
-  };
-  Ring<WT, R, NG> ring;
-  const char* base[NG][2];
-  auto point = [&](int64_t i) {
-    const int u = (int)(i / upe);
-    const int64_t f0 = (int64_t)r.expert[u] * a.F + (i % upe) * (8 * NG) + (lane >> 3);
-#pragma unroll
-    for (int g = 0; g < NG; ++g) {
-      base[g][0] = (const char*)a.w.gate + (f0 + 8 * g) * row_bytes;
-      base[g][1] = (const char*)a.w.up + (f0 + 8 * g) * row_bytes;
-    }
-  };
-  floatx4 acc[NG];
-  // chunk c of a unit; in, cn: the next visit, if there is one
-  auto visit = [&](auto more, int c, int64_t in, int cn) {
-#pragma unroll
-    for (int s = 0; s < NS; ++s) {
-#pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        u32x4 w0, w1;
-        stage_in(stage[wv], lane, ring.w[s % R][g][0], ring.w[s % R][g][1]);
-        stage_out(stage[wv], lane, w0, w1);
-        S::mma(acc[g], xs[s], w0, w1);
-      }
-      if (s + R < NS) {
-        ring.load(s + R, base, c * NS * kFewWaves, nst, row_bytes);
-      } else if constexpr (decltype(more)::value) {
-        if (s + R == NS) point(in);
-        ring.load(s + R - NS, base, cn * NS * kFewWaves, nst, row_bytes);
-      }
-      __builtin_amdgcn_sched_barrier(0);
-    }
-  };
-  point(i0);
-#pragma unroll
-  for (int s = 0; s < R; ++s) ring.load(s, base, 0, nst, row_bytes);
-  load_x(0);
-  int par = 0;
-  for (int64_t i = i0; i < i1; ++i) {
-#pragma unroll
-    for (int g = 0; g < NG; ++g) acc[g] = floatx4{0.f, 0.f, 0.f, 0.f};
-    for (int c = 0; c < nchunk; ++c) {
-      if (nchunk > 1) load_x(c);
-      const bool last = c + 1 == nchunk;
-      if (last && i + 1 == i1)
-        visit(std::false_type{}, c, 0, 0);
-      else
-        visit(std::true_type{}, c, last ? i + 1 : i, last ? 0 : c + 1);
-    }
-#pragma unroll
-    for (int g = 0; g < NG; ++g) red_put(red[par] + (wv * NG + g) * kRedWave, acc[g]);
-    __syncthreads();
-    // one half of the workgroup (NG 1: the halves take turns; NG 2: one group each) sums up;
-    // the other buffer is free until it has passed the next barrier
-    const int half = tid >> 8, g = NG == 1 ? 0 : half;
-    if (NG == 2 || half == par) {
-      const int m = (tid >> 4) & 15, n = tid & 15;
-      const int u = (int)(i / upe), f = (int)(i % upe) * (8 * NG) + 8 * g + (n & 7);
-      float v = red_get(red[par] + g * kRedWave, NG * kRedWave, m, n);
-      if (sizeof(WT) == 1)
-        v *= (n < 8 ? a.w.s_gate : a.w.s_up)[(int64_t)r.expert[u] * a.F + f];
-      const float up = __shfl_xor(v, 8, 64);
-      const uint32_t mask = r.mask[u];
-      if (n < 8 && ((mask >> m) & 1u)) {
-        const float h = v / (1.0f + expf(-v)) * up;
-        const int64_t o = (int64_t)(r.row0[u] + __popc(mask & ((1u << m) - 1))) * a.F + f;
-        if constexpr (sizeof(XT) == 4) {
-          ((float*)a.H)[o] = h;
-        } else {
-          const bf16_t hi = f32_to_bf16(h);
-          ((bf16_t*)a.H)[o] = hi;
-          a.Hlo[o] = f32_to_bf16(h - bf16_to_f32(hi));
+        for (int g = 0; g < NG; ++g) {
+          base[g][0] = (const char*)a.w.gate + (f0 + 8 * g) * row_bytes;
+          base[g][1] = (const char*)a.w.up + (f0 + 8 * g) * row_bytes;
         }
-      }
-    }
-    par ^= 1;
-  }
+        return 0;
+      },
+      [&](int64_t i, int c, u32x4 (&xs)[1][NS][S::XR]) {
+        if (nchunk == 1 && i > i0) return;   // the same for every unit
+        const int t = lane & 15;
+#pragma unroll
+        for (int s = 0; s < NS; ++s)
+#pragma unroll
+          for (int q = 0; q < S::XR; ++q) {
+            const int k = ((c * NS + s) * kFewWaves + wv) * S::SK + S::k_of(lane >> 4, q);
+            xs[0][s][q] = u32x4{0, 0, 0, 0};
+            if (t < a.T && k < a.d)
+              xs[0][s][q] = *reinterpret_cast<const u32x4*>((const XT*)a.x + (int64_t)t * a.d + k);
+          }
+      },
+      [&](int64_t i, int g, int m, int n, float v) {
+        const int u = (int)(i / upe), f = (int)(i % upe) * (8 * NG) + 8 * g + (n & 7);
+        if (sizeof(WT) == 1)
+          v *= (n < 8 ? a.w.s_gate : a.w.s_up)[(int64_t)r.expert[u] * a.F + f];
+        const float up = __shfl_xor(v, 8, 64);
+        const uint32_t mask = r.mask[u];
+        if (n < 8 && ((mask >> m) & 1u)) {
+          const float h = v / (1.0f + expf(-v)) * up;
+          const int64_t o = (int64_t)(r.row0[u] + __popc(mask & ((1u << m) - 1))) * a.F + f;
+          if constexpr (sizeof(XT) == 4) {
+            ((float*)a.H)[o] = h;
+          } else {
+            const bf16_t hi = f32_to_bf16(h);
+            ((bf16_t*)a.H)[o] = hi;
+            a.Hlo[o] = f32_to_bf16(h - bf16_to_f32(hi));
+          }
+        }
+      });
 }
 
 // Partial down products: a unit is NG x 16 rows of W_down of an expert over one chunk of F
@@ -355,99 +280,59 @@ __global__ __launch_bounds__(kFewThreads) void few_down_kernel(FewArgs a) {
   typedef typename S::X XT;
   constexpr int NH = sizeof(XT) == 4 ? 1 : 2;   // value, remainder
   __shared__ FewRoute r;
-  __shared__ __align__(16) char stage[kFewWaves][kStageBytes];
-  __shared__ float red[2][kFewWaves * NG * kRedWave];
+  __shared__ StreamLds<NG> lds;
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
   for (int i = tid; i < (int)(sizeof(FewRoute) / 4); i += kFewThreads)
     ((int*)&r)[i] = ((const int*)a.route)[i];
   __syncthreads();
   const int upc = a.d / (16 * NG);   // units per (expert, chunk)
-  int64_t i0, i1;
+  int64_t i0, i1, have = -1;
   share_of((int64_t)r.nu * a.chunks * upc, i0, i1);
-  if (i0 == i1) return;
   const int nst = (a.F + S::SK - 1) / S::SK, row_bytes = a.F * (int)sizeof(WT);
-  const int t = lane & 15, g4 = lane >> 4;
-  u32x4 xs[NH][NS][S::XR];
-  Ring<WT, NS, NG> ring;   // a whole visit in flight
-  const char* base[NG][2];
-  auto load_h = [&](int64_t uc) {
-    const int u = (int)(uc / a.chunks), c = (int)(uc % a.chunks);
-    const uint32_t mask = r.mask[u];
-    const bool mine = (mask >> t) & 1u;
-    const int64_t o = (int64_t)(r.row0[u] + __popc(mask & ((1u << t) - 1))) * a.F;
+  stream_units<WT, NS, NS, NG, NH>(
+      i0, i1, 1, nst, row_bytes, lds,
+      [&](int64_t i, const char* (&base)[NG][2]) {
+        const int64_t uc = i / upc;
+        const int64_t n0 =
+            (int64_t)r.expert[uc / a.chunks] * a.d + (i % upc) * (16 * NG) + (lane >> 3);
 #pragma unroll
-    for (int s = 0; s < NS; ++s)
+        for (int g = 0; g < NG; ++g)
 #pragma unroll
-      for (int i = 0; i < S::XR; ++i) {
-        const int k = ((c * NS + s) * kFewWaves + wv) * S::SK + S::k_of(g4, i);
+          for (int q = 0; q < 2; ++q)
+            base[g][q] = (const char*)a.w.down + (n0 + 16 * g + 8 * q) * row_bytes;
+        return (int)(uc % a.chunks) * NS * kFewWaves;
+      },
+      [&](int64_t i, int, u32x4 (&xs)[NH][NS][S::XR]) {
+        const int64_t uc = i / upc;
+        if (uc == have) return;
+        have = uc;
+        const int u = (int)(uc / a.chunks), c = (int)(uc % a.chunks), t = lane & 15;
+        const uint32_t mask = r.mask[u];
+        const bool mine = (mask >> t) & 1u;
+        const int64_t o = (int64_t)(r.row0[u] + __popc(mask & ((1u << t) - 1))) * a.F;
 #pragma unroll
-        for (int h = 0; h < NH; ++h) {
-          xs[h][s][i] = u32x4{0, 0, 0, 0};
-          if (mine && k < a.F)
-            xs[h][s][i] = *reinterpret_cast<const u32x4*>(
-                (h == 0 ? (const XT*)a.H : (const XT*)a.Hlo) + o + k);
-        }
-      }
-  };
-  int st0 = 0;
-  auto point = [&](int64_t i) {
-    const int64_t uc = i / upc;
-    st0 = (int)(uc % a.chunks) * NS * kFewWaves;
-    const int64_t n0 = (int64_t)r.expert[uc / a.chunks] * a.d + (i % upc) * (16 * NG) + (lane >> 3);
+        for (int s = 0; s < NS; ++s)
 #pragma unroll
-    for (int g = 0; g < NG; ++g)
+          for (int q = 0; q < S::XR; ++q) {
+            const int k = ((c * NS + s) * kFewWaves + wv) * S::SK + S::k_of(lane >> 4, q);
 #pragma unroll
-      for (int q = 0; q < 2; ++q)
-        base[g][q] = (const char*)a.w.down + (n0 + 16 * g + 8 * q) * row_bytes;
-  };
-  floatx4 acc[NG];
-  auto visit = [&](auto more, int64_t in) {
-    if constexpr (decltype(more)::value) point(in);
-#pragma unroll
-    for (int s = 0; s < NS; ++s) {
-#pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        u32x4 w0, w1;
-        stage_in(stage[wv], lane, ring.w[s][g][0], ring.w[s][g][1]);
-        stage_out(stage[wv], lane, w0, w1);
-#pragma unroll
-        for (int h = 0; h < NH; ++h) S::mma(acc[g], xs[h][s], w0, w1);
-      }
-      if constexpr (decltype(more)::value) ring.load(s, base, st0, nst, row_bytes);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-  };
-  point(i0);
-#pragma unroll
-  for (int s = 0; s < NS; ++s) ring.load(s, base, st0, nst, row_bytes);
-  int par = 0;
-  int64_t have = -1;
-  for (int64_t i = i0; i < i1; ++i) {
-    const int64_t uc = i / upc;
-    if (uc != have) load_h(have = uc);
-#pragma unroll
-    for (int g = 0; g < NG; ++g) acc[g] = floatx4{0.f, 0.f, 0.f, 0.f};
-    if (i + 1 == i1)
-      visit(std::false_type{}, 0);
-    else
-      visit(std::true_type{}, i + 1);
-#pragma unroll
-    for (int g = 0; g < NG; ++g) red_put(red[par] + (wv * NG + g) * kRedWave, acc[g]);
-    __syncthreads();
-    const int half = tid >> 8, g = NG == 1 ? 0 : half;
-    if (NG == 2 || half == par) {
-      const int m = (tid >> 4) & 15, u = (int)(uc / a.chunks);
-      const int n = (int)(i % upc) * (16 * NG) + 16 * g + (tid & 15);
-      const uint32_t mask = r.mask[u];
-      if ((mask >> m) & 1u) {
-        float v = red_get(red[par] + g * kRedWave, NG * kRedWave, m, tid & 15);
+            for (int h = 0; h < NH; ++h) {
+              xs[h][s][q] = u32x4{0, 0, 0, 0};
+              if (mine && k < a.F)
+                xs[h][s][q] = *reinterpret_cast<const u32x4*>(
+                    (h == 0 ? (const XT*)a.H : (const XT*)a.Hlo) + o + k);
+            }
+          }
+      },
+      [&](int64_t i, int g, int m, int q, float v) {
+        const int64_t uc = i / upc;
+        const int u = (int)(uc / a.chunks), n = (int)(i % upc) * (16 * NG) + 16 * g + q;
+        const uint32_t mask = r.mask[u];
+        if (!((mask >> m) & 1u)) return;
         if (sizeof(WT) == 1) v *= a.w.s_down[(int64_t)r.expert[u] * a.d + n];
         const int64_t row = r.row0[u] + __popc(mask & ((1u << m) - 1));
         a.part[(row * a.chunks + uc % a.chunks) * a.d + n] = v;
-      }
-    }
-    par ^= 1;
-  }
+      });
 }
 
 // y_t = sum over slots of w (sum over chunks), the shared expert, the residual.

@@ -112,42 +112,59 @@ __device__ __forceinline__ void store8(const LinearArgs& a, int64_t i, const flo
 }
 
 // ------------------------------------------------------------------ at most 16 rows
-// A workgroup streams 16 weight rows (gated: 8 gate rows and the 8 matching up rows) over the
-// whole of K, split over its waves.
-template <typename WT, bool GATED>
+// A unit is NG x 16 weight rows (gated: NG x 8 gate rows and the 8 matching up rows).
+template <typename WT, int NS, int R, int NG, bool GATED>
 __global__ __launch_bounds__(kStreamThreads) void linear_rows_kernel(LinearArgs a) {
   typedef Stream<WT> S;
   typedef typename S::X XT;
-  __shared__ __align__(16) char stage[kStreamWaves][kStageBytes];
-  __shared__ float red[kStreamWaves * kRedWave];
-  constexpr int COLS = GATED ? 8 : 16;
-  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, t = lane & 15;
-  const int n0 = blockIdx.x * COLS;
-  const char* row[2];
+  __shared__ StreamLds<NG> lds;
+  constexpr int COLS = GATED ? 8 : 16;   // output columns of a group
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  int64_t i0, i1;
+  share_of((a.N + COLS * NG - 1) / (COLS * NG), i0, i1);
+  const int nst = (a.K + S::SK - 1) / S::SK;
+  const int nchunk = (nst + NS * kStreamWaves - 1) / (NS * kStreamWaves);
+  stream_units<WT, NS, R, NG, 1>(
+      i0, i1, nchunk, nst, a.K * (int)sizeof(WT), lds,
+      [&](int64_t i, const char* (&base)[NG][2]) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
-    row[i] = (const char*)a.W[GATED ? i : 0] +
-             (int64_t)min(n0 + (GATED ? 0 : 8 * i) + (lane >> 3), a.N - 1) * a.ldw * (int)sizeof(WT);
-  const XT* x = (const XT*)a.x + (int64_t)min(t, a.M - 1) * a.ldx;
-  floatx4 acc = {0.f, 0.f, 0.f, 0.f};
-  stream_rows<WT, 8>(acc, stage[wv], a.K, [&](int i, int byte) { return row[i] + byte; },
-                     [&](int k) { return t < a.M ? x + k : nullptr; });
-  red_put(red + wv * kRedWave, acc);
-  __syncthreads();
-  if (tid >= 256) return;
-  const int m = tid >> 4, q = tid & 15;
-  const int n = n0 + (GATED ? q & 7 : q), nc = min(n, a.N - 1), mat = GATED ? q >> 3 : 0;
-  float v = biased(scaled(red_get(red, kRedWave, m, q), a.scale[mat], nc), a.bias[mat], nc);
-  if constexpr (GATED) {
-    const float up = __shfl_xor(v, 8, 64);
-    v = act_f(v, a.act) * up;
-    if (q >= 8) return;
-  } else {
-    v = act_f(v, a.act);
-  }
-  if (m >= a.M || n >= a.N) return;
-  if (a.residual) v += load_out(a, a.residual, m * a.ldr + n);
-  store_out(a, m * a.ldo + n, v);
+        for (int g = 0; g < NG; ++g)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int n = (int)i * COLS * NG + COLS * g + (GATED ? 0 : 8 * h) + (lane >> 3);
+            base[g][h] = (const char*)a.W[GATED ? h : 0] +
+                         min(n, a.N - 1) * a.ldw * (int)sizeof(WT);
+          }
+        return 0;
+      },
+      [&](int64_t i, int c, u32x4 (&xs)[1][NS][S::XR]) {
+        if (nchunk == 1 && i > i0) return;   // the same for every unit
+        const int t = lane & 15;
+#pragma unroll
+        for (int s = 0; s < NS; ++s)
+#pragma unroll
+          for (int q = 0; q < S::XR; ++q) {
+            const int k = ((c * NS + s) * kStreamWaves + wv) * S::SK + S::k_of(lane >> 4, q);
+            xs[0][s][q] = u32x4{0, 0, 0, 0};
+            if (t < a.M && k < a.K)
+              xs[0][s][q] = *reinterpret_cast<const u32x4*>((const XT*)a.x + t * a.ldx + k);
+          }
+      },
+      [&](int64_t i, int g, int m, int q, float v) {
+        const int n = (int)i * COLS * NG + COLS * g + (GATED ? q & 7 : q);
+        const int nc = min(n, a.N - 1), mat = GATED ? q >> 3 : 0;
+        v = biased(scaled(v, a.scale[mat], nc), a.bias[mat], nc);
+        if constexpr (GATED) {
+          const float up = __shfl_xor(v, 8, 64);
+          v = act_f(v, a.act) * up;
+          if (q >= 8) return;
+        } else {
+          v = act_f(v, a.act);
+        }
+        if (m >= a.M || n >= a.N) return;
+        if (a.residual) v += load_out(a, a.residual, m * a.ldr + n);
+        store_out(a, m * a.ldo + n, v);
+      });
 }
 
 // ------------------------------------------------------------------ MFMA tiles
@@ -419,8 +436,10 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearArgs a)
 #pragma unroll
       for (int i = 0; i < WB; ++i) wo[i] = TT::operand(wf[buf][i]);
       // Operand reads of the next slice (past the last step: stale, unused) go out one by one
-      // between the MFMAs, in whose shadow they issue.
-      constexpr int B = XB * WB, RD = XB + WB, EVERY = B >= 2 * RD ? 2 : 1;
+      // between the MFMAs, in whose shadow they issue; so do the loads, of slots in the first
+      // half of their slice (LF = 2: gated 4096-row product 760 -> 727 us; whole stages have
+      // time to land and prefer an even spread, 213 against 216 us for 2048 x 4096 x 14336).
+      constexpr int B = XB * WB, RD = XB + WB, EVERY = B >= 2 * RD ? 2 : 1, LF = 4;
       static_assert(RD <= B, "a read per MFMA at most");
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -439,16 +458,16 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearArgs a)
             if constexpr (SLOTS) {
               if (s == 0) {   // x part of step t + 2
 #pragma unroll
-                for (int l = q * NX / B; l < (q + 1) * NX / B; ++l)
+                for (int l = q * LF * NX / B; l < min((q + 1) * LF * NX / B, NX); ++l)
                   load(std::false_type{}, l, t + 2, part_after(nx, 2));
               } else {
 #pragma unroll
-                for (int l = q * NW / B; l < (q + 1) * NW / B; ++l)
+                for (int l = q * LF * NW / B; l < min((q + 1) * LF * NW / B, NW); ++l)
                   load(std::false_type{}, NX + l, t + 2, px);
               }
             } else if (s == 1) {
 #pragma unroll
-              for (int l = q * L / B; l < (q + 1) * L / B; ++l)
+              for (int l = q * LF * L / B; l < min((q + 1) * LF * L / B, L); ++l)
                 load(std::false_type{}, l, t + ST, l < NX ? px : pw);
             }
           }
@@ -557,14 +576,36 @@ static hipError_t run_tiles(const LinearArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+template <typename WT, int NS, int R, int NG, bool GATED>
+static hipError_t run_rows(const LinearArgs& a, hipStream_t s) {
+  const int64_t units = ceil_div(a.N, (GATED ? 8 : 16) * NG);
+  hipLaunchKernelGGL((linear_rows_kernel<WT, NS, R, NG, GATED>),
+                     dim3((unsigned)std::min<int64_t>(units, device_cu_count())),
+                     dim3(kStreamThreads), 0, s, a);
+  return hipGetLastError();
+}
+
+// At most 16 rows: the least number of steps per wave that holds K, so that the token operand
+// stays in registers (K beyond the last runs in chunks).
+template <typename WT, bool GATED>
+static hipError_t launch_rows(const LinearArgs& a, hipStream_t s) {
+  const int64_t per = ceil_div(ceil_div(a.K, Stream<WT>::SK), kStreamWaves);
+  if constexpr (sizeof(WT) == 1) {
+    if (per <= 1) return run_rows<WT, 1, 1, 2, GATED>(a, s);
+    if (per <= 2) return run_rows<WT, 2, 2, 2, GATED>(a, s);
+    if (per <= 4) return run_rows<WT, 4, 4, 2, GATED>(a, s);
+    return run_rows<WT, 8, 4, 1, GATED>(a, s);
+  } else {
+    if (per <= 2) return run_rows<WT, 2, 2, 1, GATED>(a, s);
+    if (per <= 4) return run_rows<WT, 4, 4, 1, GATED>(a, s);
+    if (per <= 8) return run_rows<WT, 8, 8, 1, GATED>(a, s);
+    return run_rows<WT, 14, 7, 1, GATED>(a, s);
+  }
+}
+
 template <typename WT, bool GATED>
 static hipError_t launch_linear_t(const LinearArgs& a, hipStream_t s) {
-  if (a.M <= 16) {
-    hipLaunchKernelGGL((linear_rows_kernel<WT, GATED>),
-                       dim3((unsigned)ceil_div(a.N, GATED ? 8 : 16)), dim3(kStreamThreads), 0, s,
-                       a);
-    return hipGetLastError();
-  }
+  if (a.M <= 16) return launch_rows<WT, GATED>(a, s);
   // Largest tile (x rows by weight rows) that still gives every CU one; below that, what gives
   // the most.  Tiles taller than 64 address their rows from the first with 32 bits.
   const int64_t cus = device_cu_count(), out = GATED ? 2 : 1;

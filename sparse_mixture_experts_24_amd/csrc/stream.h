@@ -17,6 +17,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "moe_internal.h"
 
 namespace moe {
@@ -168,6 +170,108 @@ __device__ __forceinline__ float red_get(const float* red, int red_stride, int m
 #pragma unroll
   for (int q = 1; q < kStreamWaves; ++q) v += red[q * red_stride + m * kRedLd + n];
   return v;
+}
+
+// A workgroup's run of consecutive units of n, as even as they go.
+__device__ inline void share_of(int64_t n, int64_t& i0, int64_t& i1) {
+  i0 = n * blockIdx.x / gridDim.x;
+  i1 = n * (blockIdx.x + 1) / gridDim.x;
+}
+
+// LDS of stream_units.
+template <int NG>
+struct StreamLds {
+  __align__(16) char stage[kStreamWaves][kStageBytes];
+  float red[2][kStreamWaves * NG * kRedWave];
+};
+
+// Units i0 .. i1 - 1 of NG x 16 weight rows each, against a token operand that stays in
+// registers while it can.  A unit is visited once per chunk of NS steps per wave (NS x 8
+// steps of the row; one chunk where the row is no longer).  A ring of R steps (R divides
+// NS) runs across the visits: as step s is used, step s + R goes out, of this visit or of
+// the next, so a wave always has R NG 2 KB in flight.
+//   point(i, base)       base[g][h]: the lane's row of load h of group g; returns the row's
+//                        first step
+//   load_x(i, c, xs)     the wave's token operand of chunk c, xs[0 .. NH - 1] multiplied by
+//                        the same weights (only called where it may have changed)
+//   done(i, g, m, n, v)  sum v of token m and row n of group g, called by 256 threads (whole
+//                        waves) for each group; ends the unit
+//   nst, row_bytes       steps and bytes of a weight row
+// Steps past nst repeat its last one and bytes past the row its last chunk (cache hits); the
+// token operand must be zero there.
+template <typename WT, int NS, int R, int NG, int NH, typename Point, typename LoadX,
+          typename Done>
+__device__ __forceinline__ void stream_units(int64_t i0, int64_t i1, int nchunk, int nst,
+                                             int row_bytes, StreamLds<NG>& lds, Point point,
+                                             LoadX load_x, Done done) {
+  typedef Stream<WT> S;
+  static_assert(NS % R == 0, "ring slots keep their steps");
+  if (i0 >= i1) return;
+  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+  char* stage = lds.stage[wv];
+  u32x4 xs[NH][NS][S::XR], ring[R][NG][2];
+  const char* base[NG][2];
+  auto load = [&](int s, int st0) {
+    const int st = min(st0 + s * kStreamWaves + wv, nst - 1);
+    const int byte = min(st * kStepBytes + 16 * (lane & 7), row_bytes - 16);
+#pragma unroll
+    for (int g = 0; g < NG; ++g)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        ring[s % R][g][h] = *reinterpret_cast<const u32x4*>(base[g][h] + byte);
+  };
+  floatx4 acc[NG];
+  int first = point(i0, base);   // of the unit that base points to
+  // Chunk c of a unit; in, cn: the next visit, if there is one.
+  auto visit = [&](auto more, int c, int64_t in, int cn) {
+    const int st0 = first + c * NS * kStreamWaves;
+    int stn = 0;
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        u32x4 w0, w1;
+        stage_in(stage, lane, ring[s % R][g][0], ring[s % R][g][1]);
+        stage_out(stage, lane, w0, w1);
+#pragma unroll
+        for (int h = 0; h < NH; ++h) S::mma(acc[g], xs[h][s], w0, w1);
+      }
+      if (s + R < NS) {
+        load(s + R, st0);
+      } else if constexpr (decltype(more)::value) {
+        if (s + R == NS) {
+          first = point(in, base);
+          stn = first + cn * NS * kStreamWaves;
+        }
+        load(s + R - NS, stn);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+#pragma unroll
+  for (int s = 0; s < R; ++s) load(s, first);
+  int par = 0;
+  for (int64_t i = i0; i < i1; ++i) {
+#pragma unroll
+    for (int g = 0; g < NG; ++g) acc[g] = floatx4{0.f, 0.f, 0.f, 0.f};
+    for (int c = 0; c < nchunk; ++c) {
+      load_x(i, c, xs);
+      const bool last = c + 1 == nchunk;
+      if (last && i + 1 == i1)
+        visit(std::false_type{}, c, 0, 0);
+      else
+        visit(std::true_type{}, c, last ? i + 1 : i, last ? 0 : c + 1);
+    }
+#pragma unroll
+    for (int g = 0; g < NG; ++g) red_put(lds.red[par] + (wv * NG + g) * kRedWave, acc[g]);
+    __syncthreads();
+    // one half of the workgroup (NG 1: the halves take turns; NG 2: one group each) sums up;
+    // the other buffer is free until it has passed the next barrier
+    const int half = tid >> 8, g = NG == 1 ? 0 : half, m = (tid >> 4) & 15, n = tid & 15;
+    if (NG == 2 || half == par)
+      done(i, g, m, n, red_get(lds.red[par] + g * kRedWave, NG * kRedWave, m, n));
+    par ^= 1;
+  }
 }
 
 }  // namespace moe
