@@ -8,6 +8,7 @@
 // the stable rank of an assignment is the number of lower tokens in the set.
 #include <math.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "moe_internal.h"
@@ -30,12 +31,13 @@ struct FewArgs {
   void* out;
   float* f;
   float* p;
-  float* logits;     // [T, E]
+  float* logits;     // [ks, T, E] partial sums
   FewRoute* route;   // the routing, for the kernels after the first expert kernel
   void* H;           // [T*k + S*T, F] expert-contiguous rows: float, or bf16 values
   bf16_t* Hlo;       //   and (bf16 layers) the bf16 remainders
   float* part;       // [T*k + S*T, chunks, d] partial down products
   int T, d, E, F, k, S, C;   // C: capacity, -1 none
+  int ks;            // parts that the logits are summed in
   int chunks;        // parts that the down products' F range is summed in
 };
 
@@ -56,24 +58,32 @@ __device__ inline float wide(const uint8_t* p) { return __builtin_amdgcn_cvt_f32
 __device__ inline void narrow(float* p, float v) { *p = v; }
 __device__ inline void narrow(bf16_t* p, float v) { *p = f32_to_bf16(v); }
 
-// Softmax, top-k, capacity and the touched experts from the logits, by one workgroup.
-// Block 0 also writes f and P.  Ends with a barrier.
-__device__ inline void few_route(const FewArgs& a, FewRoute& r) {
-  __shared__ uint32_t chosen[kMaxExperts];    // token set of each expert
-  __shared__ float psum[kFewWaves][kMaxExperts];
-  __shared__ int16_t sel[kFew][kMaxTopK];
-  constexpr int NV = kMaxExperts / 64;
-  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
-  const int nv = (a.E + 63) / 64;
-  for (int e = tid; e < kMaxExperts; e += kFewThreads) chosen[e] = 0;
-  float ps[NV] = {};
-  __syncthreads();
+// What the routing needs of LDS while it is formed.
+struct RouteLds {
+  uint32_t chosen[kMaxExperts];   // token set of each expert
+  float psum[kFewWaves][kMaxExperts];
+  int16_t sel[kFew][kMaxTopK];
+};
+
+// Softmax and top-k of the wave's tokens, at most NV experts per lane.
+template <int NV>
+__device__ __forceinline__ void route_tokens(const FewArgs& a, FewRoute& r, RouteLds& l) {
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  float bias[NV], ps[NV] = {};
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+    bias[i] = a.bias && lane + 64 * i < a.E ? a.bias[lane + 64 * i] : 0.0f;
   for (int t = wv; t < a.T; t += kFewWaves) {
     float v[NV], s[NV], m = -INFINITY, sum = 0.0f;
 #pragma unroll
+    for (int i = 0; i < NV; ++i) v[i] = 0.0f;
+    for (int q = 0; q < a.ks; ++q)   // the logits' partial sums, in order
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (lane + 64 * i < a.E) v[i] += a.logits[(q * a.T + t) * a.E + lane + 64 * i];
+#pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int e = lane + 64 * i;
-      v[i] = e < a.E ? a.logits[t * a.E + e] : -INFINITY;
+      if (lane + 64 * i >= a.E) v[i] = -INFINITY;
       m = fmaxf(m, v[i]);
     }
     m = wave_max(m);
@@ -85,10 +95,9 @@ __device__ inline void few_route(const FewArgs& a, FewRoute& r) {
     sum = wave_sum(sum);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int e = lane + 64 * i;
       v[i] /= sum;   // p
       ps[i] += v[i];
-      s[i] = e < a.E ? v[i] + (a.bias ? a.bias[e] : 0.0f) : -INFINITY;
+      s[i] = lane + 64 * i < a.E ? v[i] + bias[i] : -INFINITY;
     }
     unsigned taken = 0;
     float tot = 0.0f, mine = 0.0f;
@@ -98,34 +107,54 @@ __device__ inline void few_route(const FewArgs& a, FewRoute& r) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int e = lane + 64 * i;
-        if (i < nv && e < a.E && !((taken >> i) & 1u)) take_better(bv, be, s[i], e);
+        const bool free = (e < a.E) & !((taken >> i) & 1u);
+        take_better(bv, be, free ? s[i] : -INFINITY, free ? e : 0x7fffffff);
       }
       wave_argmax(bv, be);
       const bool ok = (unsigned)be < (unsigned)a.E;   // false only for non-finite scores
       float pp = 0.0f;
 #pragma unroll
       for (int i = 0; i < NV; ++i) pp = ok && i == (be >> 6) ? v[i] : pp;
-      pp = __shfl(pp, be & 63, 64);
+      pp = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(pp), be & 63));
       if (ok && lane == (be & 63)) taken |= 1u << (be >> 6);
       tot += pp;
       mine = lane == j ? pp : mine;
       if (lane == 0) {
-        sel[t][j] = ok ? (int16_t)be : (int16_t)-1;
-        if (ok) atomicOr(&chosen[be], 1u << t);
+        l.sel[t][j] = ok ? (int16_t)be : (int16_t)-1;
+        if (ok) atomicOr(&l.chosen[be], 1u << t);
       }
     }
     if (lane < a.k) r.w[t][lane] = mine / tot;
   }
+  if (blockIdx.x == 0) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i) psum[wv][lane + 64 * i] = ps[i];
+    for (int i = 0; i < NV; ++i) l.psum[wv][lane + 64 * i] = ps[i];
+  }
+}
+
+// Softmax, top-k, capacity and the touched experts from the logits, by one workgroup.
+// Block 0 also writes f and P.  Ends with a barrier.
+__device__ inline void few_route(const FewArgs& a, FewRoute& r, RouteLds& l) {
+  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+  const int nv = (a.E + 63) / 64;
+  uint32_t* chosen = l.chosen;
+  for (int e = tid; e < 64 * nv; e += kFewThreads) chosen[e] = 0;
+  __syncthreads();
+  if (nv == 1)
+    route_tokens<1>(a, r, l);
+  else if (nv <= 4)
+    route_tokens<4>(a, r, l);
+  else
+    route_tokens<8>(a, r, l);
   __syncthreads();
   if (blockIdx.x == 0) {
     for (int e = tid; e < a.E; e += kFewThreads) {
       float v = 0.0f;
-      for (int q = 0; q < kFewWaves; ++q) v += psum[q][e];
+      for (int q = 0; q < kFewWaves; ++q) v += l.psum[q][e];
       if (a.f) a.f[e] = (float)((double)__popc(chosen[e]) / (double)(a.T * a.k));
       if (a.p) a.p[e] = v / (float)a.T;
     }
+    __syncthreads();   // wave 0 reuses chosen below
   }
   // The first C tokens of each expert are kept; experts with rows are listed in order, 64
   // experts at a time by wave 0.
@@ -172,7 +201,7 @@ __device__ inline void few_route(const FewArgs& a, FewRoute& r) {
     const int t = i / (a.k + 1), j = i % (a.k + 1);
     int row = -1;
     if (j < a.k) {
-      const int e = sel[t][j];
+      const int e = l.sel[t][j];
       if (e >= 0) {
         const uint32_t c = chosen[e];
         if ((c >> t) & 1u) row = (int)(c >> 16) + __popc(c & ((1u << t) - 1));
@@ -185,7 +214,7 @@ __device__ inline void few_route(const FewArgs& a, FewRoute& r) {
   __syncthreads();
 }
 
-// Router logits of 16 experts per workgroup.
+// Router logits of 16 experts (blockIdx.x) over one part of d (blockIdx.y).
 template <typename XT>
 __global__ __launch_bounds__(kFewThreads) void few_logits_kernel(FewArgs a) {
   __shared__ __align__(16) char stage[kFewWaves][kStageBytes];
@@ -198,13 +227,16 @@ __global__ __launch_bounds__(kFewThreads) void few_logits_kernel(FewArgs a) {
   for (int i = 0; i < 2; ++i)
     row[i] = (const char*)a.Wr +
              (int64_t)min(e0 + 8 * i + (lane >> 3), a.E - 1) * a.d * (int)sizeof(XT);
+  const int nst = a.d / Stream<XT>::SK;
+  const int st0 = nst * blockIdx.y / a.ks, st1 = nst * (blockIdx.y + 1) / a.ks;
   floatx4 acc = {0.f, 0.f, 0.f, 0.f};
-  stream_rows<XT, 8>(acc, stage[wv], a.d, [&](int i, int byte) { return row[i] + byte; },
+  stream_rows<XT, 4>(acc, stage[wv], st0, st1, [&](int i, int byte) { return row[i] + byte; },
                      [&](int k) { return t < a.T ? x + k : nullptr; });
   red_put(red + wv * kRedWave, acc);
   __syncthreads();
   const int m = tid >> 4, n = tid & 15;
-  if (m < a.T && e0 + n < a.E) a.logits[m * a.E + e0 + n] = red_get(red, kRedWave, m, n);
+  if (m < a.T && e0 + n < a.E)
+    a.logits[((int)blockIdx.y * a.T + m) * a.E + e0 + n] = red_get(red, kRedWave, m, n);
 }
 
 // h = SiLU(x W_gate^T) * (x W_up^T).  A unit is NG x (8 gate rows and the 8 matching up
@@ -215,15 +247,16 @@ __global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(FewArgs a) {
   typedef Stream<WT> S;
   typedef typename S::X XT;
   __shared__ FewRoute r;
+  __shared__ RouteLds rl;
   __shared__ StreamLds<NG> lds;
-  few_route(a, r);
+  few_route(a, r, rl);
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
   if (blockIdx.x == 0)
     for (int i = tid; i < (int)(sizeof(FewRoute) / 4); i += kFewThreads)
       ((int*)a.route)[i] = ((const int*)&r)[i];
   const int upe = a.F / (8 * NG);   // units per expert
   int64_t i0, i1;
-  share_of((int64_t)r.nu * upe, i0, i1);
+  share_of((int64_t)r.nu * upe, blockIdx.x, gridDim.x, i0, i1);
   const int nst = (a.d + S::SK - 1) / S::SK, row_bytes = a.d * (int)sizeof(WT);
   const int nchunk = (nst + NS * kFewWaves - 1) / (NS * kFewWaves);
   stream_units<WT, NS, R, NG, 1>(
@@ -287,7 +320,7 @@ __global__ __launch_bounds__(kFewThreads) void few_down_kernel(FewArgs a) {
   __syncthreads();
   const int upc = a.d / (16 * NG);   // units per (expert, chunk)
   int64_t i0, i1, have = -1;
-  share_of((int64_t)r.nu * a.chunks * upc, i0, i1);
+  share_of((int64_t)r.nu * a.chunks * upc, blockIdx.x, gridDim.x, i0, i1);
   const int nst = (a.F + S::SK - 1) / S::SK, row_bytes = a.F * (int)sizeof(WT);
   stream_units<WT, NS, NS, NG, NH>(
       i0, i1, 1, nst, row_bytes, lds,
@@ -365,6 +398,13 @@ struct FewWorkspace {
   size_t bytes;
 };
 
+// Parts of d that the logits are summed in: one or two steps per wave each, as long as a
+// workgroup's routing reads at most 1024 partial sums per token.
+static int64_t logit_parts(const moe_desc_t& d) {
+  const int64_t steps = d.d_model / (d.dtype == MOE_DTYPE_F32 ? Stream<float>::SK : Stream<bf16_t>::SK);
+  return std::min(ceil_div(steps, 2 * kFewWaves), std::max<int64_t>(1, 1024 / d.n_experts));
+}
+
 // Elements of F in a chunk of the down products: a wave's NS steps times the waves.
 constexpr int kDownSteps = 4;
 static int64_t down_chunks(const moe_desc_t& d, bool fp8) {
@@ -383,7 +423,7 @@ static FewWorkspace carve_few(const moe_desc_t& d, void* base) {
   };
   FewWorkspace w{};
   const int64_t rows = d.T * d.top_k + d.n_shared * d.T;
-  w.logits = (float*)take(d.T * d.n_experts * 4);
+  w.logits = (float*)take(logit_parts(d) * d.T * d.n_experts * 4);
   w.route = (FewRoute*)take(sizeof(FewRoute));
   w.H = take(rows * d.d_ff * (d.dtype == MOE_DTYPE_F32 ? 4 : 2));
   w.Hlo = (bf16_t*)take(d.dtype == MOE_DTYPE_F32 ? 0 : rows * d.d_ff * 2);
@@ -409,7 +449,7 @@ template <typename WT, typename OT>
 static hipError_t launch_few(const FewArgs& a, hipStream_t s) {
   typedef typename Stream<WT>::X XT;
   const int per = (int)ceil_div(ceil_div(a.d, Stream<WT>::SK), kFewWaves);   // steps per wave
-  hipLaunchKernelGGL(few_logits_kernel<XT>, dim3((unsigned)ceil_div(a.E, 16)), dim3(kFewThreads),
+  hipLaunchKernelGGL(few_logits_kernel<XT>, dim3((unsigned)ceil_div(a.E, 16), a.ks), dim3(kFewThreads),
                      0, s, a);
   if constexpr (sizeof(WT) == 1) {
     if (per <= 1)
@@ -489,6 +529,7 @@ static moe_status_t few_impl(const moe_desc_t* desc, const void* x, const void* 
                   (int)d.top_k,
                   (int)d.n_shared,
                   (int)capacity_of(d),
+                  (int)logit_parts(d),
                   (int)down_chunks(d, ew.fp8)};
   const bool of32 = d.out_dtype == MOE_DTYPE_F32;
   hipError_t e;

@@ -121,7 +121,7 @@ __global__ __launch_bounds__(kStreamThreads) void linear_rows_kernel(LinearArgs 
   constexpr int COLS = GATED ? 8 : 16;   // output columns of a group
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
   int64_t i0, i1;
-  share_of((a.N + COLS * NG - 1) / (COLS * NG), i0, i1);
+  share_of((a.N + COLS * NG - 1) / (COLS * NG), blockIdx.x, gridDim.x, i0, i1);
   const int nst = (a.K + S::SK - 1) / S::SK;
   const int nchunk = (nst + NS * kStreamWaves - 1) / (NS * kStreamWaves);
   stream_units<WT, NS, R, NG, 1>(

@@ -108,52 +108,38 @@ __device__ __forceinline__ void stage_out(const char* buf, int lane, u32x4& w0, 
   w1 = *reinterpret_cast<const u32x4*>(buf + r * kStepBytes + 16 * ((2 * g + 1) ^ (r >> 1)));
 }
 
-// The wave's part of one product over whole rows: w_at(i, chunk byte) gives the address of
-// load i (rows lane / 8, 8 + lane / 8) at a byte of the row, x_at(k) the lane's token operand
-// at element k (or nullptr: zero).  R steps are in flight; past the wave's last step the
-// loads repeat it (cache hits, never used).  Elements from K on are zero in the token operand
-// and some valid element of the row in the weights.
+// The wave's part of one product over steps st0 .. st1 - 1, all within the rows: w_at(i, byte)
+// gives the address of load i (rows lane / 8, 8 + lane / 8) at a byte of the row, x_at(k) the
+// lane's token operand at element k (or nullptr: zero).  R steps are loaded at a time.
 template <typename WT, int R, typename WAt, typename XAt>
-__device__ __forceinline__ void stream_rows(floatx4& acc, char* buf, int K, WAt w_at, XAt x_at) {
+__device__ __forceinline__ void stream_rows(floatx4& acc, char* buf, int st0, int st1, WAt w_at,
+                                            XAt x_at) {
   typedef Stream<WT> S;
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, g = lane >> 4;
-  const int nst = (K + S::SK - 1) / S::SK;
-  const int nj = (nst - wv + kStreamWaves - 1) / kStreamWaves;
-  if (nj <= 0) return;
-  const int row_bytes = K * (int)sizeof(WT);
-  u32x4 w[R][2], x[R][S::XR];
-  auto load = [&](int q, int j) {
-    const int st = wv + kStreamWaves * min(j, nj - 1);
-    const int byte = min(st * kStepBytes + 16 * (lane & 7), row_bytes - 16);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) w[q][i] = *reinterpret_cast<const u32x4*>(w_at(i, byte));
-#pragma unroll
-    for (int i = 0; i < S::XR; ++i) {
-      const int k = st * S::SK + S::k_of(g, i);
-      const auto* p = k < K ? x_at(k) : nullptr;
-      x[q][i] = p ? *reinterpret_cast<const u32x4*>(p) : u32x4{0, 0, 0, 0};
-    }
-  };
-  auto use = [&](int q) {
-    u32x4 w0, w1;
-    stage_in(buf, lane, w[q][0], w[q][1]);
-    stage_out(buf, lane, w0, w1);
-    S::mma(acc, x[q], w0, w1);
-  };
-#pragma unroll
-  for (int q = 0; q < R - 1; ++q) load(q, q);
-  int j0 = 0;
-  for (; j0 + R <= nj; j0 += R) {
+  for (int j = st0 + wv; j < st1; j += R * kStreamWaves) {
+    u32x4 w[R][2], x[R][S::XR];
 #pragma unroll
     for (int q = 0; q < R; ++q) {
-      load((q + R - 1) % R, j0 + q + R - 1);
-      __builtin_amdgcn_sched_barrier(0);   // the loads stay ahead of the products
-      use(q);
+      const int st = j + q * kStreamWaves;
+      if (st >= st1) break;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        w[q][i] = *reinterpret_cast<const u32x4*>(w_at(i, st * kStepBytes + 16 * (lane & 7)));
+#pragma unroll
+      for (int i = 0; i < S::XR; ++i) {
+        const auto* p = x_at(st * S::SK + S::k_of(g, i));
+        x[q][i] = p ? *reinterpret_cast<const u32x4*>(p) : u32x4{0, 0, 0, 0};
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+      if (j + q * kStreamWaves >= st1) break;
+      u32x4 w0, w1;
+      stage_in(buf, lane, w[q][0], w[q][1]);
+      stage_out(buf, lane, w0, w1);
+      S::mma(acc, x[q], w0, w1);
     }
   }
-#pragma unroll
-  for (int q = 0; q < R - 1; ++q)
-    if (j0 + q < nj) use(q);
 }
 
 // The waves' 16 x 16 partial products, summed in wave order.  Row stride 20 floats: the four
@@ -172,10 +158,10 @@ __device__ __forceinline__ float red_get(const float* red, int red_stride, int m
   return v;
 }
 
-// A workgroup's run of consecutive units of n, as even as they go.
-__device__ inline void share_of(int64_t n, int64_t& i0, int64_t& i1) {
-  i0 = n * blockIdx.x / gridDim.x;
-  i1 = n * (blockIdx.x + 1) / gridDim.x;
+// Share s of `of`: a run of consecutive units of n, the shares as even as they go.
+__device__ inline void share_of(int64_t n, int s, int of, int64_t& i0, int64_t& i1) {
+  i0 = n * s / of;
+  i1 = n * (s + 1) / of;
 }
 
 // LDS of stream_units.
