@@ -239,39 +239,39 @@ __global__ __launch_bounds__(kFewThreads) void few_logits_kernel(FewArgs a) {
     a.logits[((int)blockIdx.y * a.T + m) * a.E + e0 + n] = red_get(red, kRedWave, m, n);
 }
 
-// h = SiLU(x W_gate^T) * (x W_up^T).  A unit is NG x (8 gate rows and the 8 matching up
-// rows) of a touched expert; all T tokens run through it (the matrix cores have the room),
-// and the rows of the tokens that chose the expert are kept.
-template <typename WT, int NS, int R, int NG>
+// h = SiLU(x W_gate^T) * (x W_up^T).  A unit is 8 gate rows and the 8 matching up rows of a
+// touched expert; all T tokens run through it (the matrix cores have the room), and the
+// rows of the tokens that chose the expert are kept.
+template <typename WT, int NS, int R>
 __global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(FewArgs a) {
   typedef Stream<WT> S;
   typedef typename S::X XT;
   __shared__ FewRoute r;
-  __shared__ RouteLds rl;
-  __shared__ StreamLds<NG> lds;
-  few_route(a, r, rl);
+  __shared__ union {
+    RouteLds route;
+    StreamLds<R> stream;
+  } lds;
+  few_route(a, r, lds.route);
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
   if (blockIdx.x == 0)
     for (int i = tid; i < (int)(sizeof(FewRoute) / 4); i += kFewThreads)
       ((int*)a.route)[i] = ((const int*)&r)[i];
-  const int upe = a.F / (8 * NG);   // units per expert
-  int64_t i0, i1;
+  const int upe = a.F / 8;   // units per expert
+  int i0, i1;
   share_of((int64_t)r.nu * upe, blockIdx.x, gridDim.x, i0, i1);
   const int nst = (a.d + S::SK - 1) / S::SK, row_bytes = a.d * (int)sizeof(WT);
   const int nchunk = (nst + NS * kFewWaves - 1) / (NS * kFewWaves);
-  stream_units<WT, NS, R, NG, 1>(
-      i0, i1, nchunk, nst, row_bytes, lds,
-      [&](int64_t i, const char* (&base)[NG][2]) {
-        const int u = (int)(i / upe);
-        const int64_t f0 = (int64_t)r.expert[u] * a.F + (i % upe) * (8 * NG) + (lane >> 3);
-#pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          base[g][0] = (const char*)a.w.gate + (f0 + 8 * g) * row_bytes;
-          base[g][1] = (const char*)a.w.up + (f0 + 8 * g) * row_bytes;
-        }
+  stream_units<WT, NS, R, 1>(
+      i0, i1, nchunk, nst, row_bytes, lds.stream,
+      [&](int i, UnitRows& rows) {
+        const int u = i / upe;
+        const int64_t f0 = (int64_t)r.expert[u] * a.F + i % upe * 8;
+        rows.base[0] = uniform((const char*)a.w.gate + f0 * row_bytes);
+        rows.base[1] = uniform((const char*)a.w.up + f0 * row_bytes);
+        rows.off[0] = rows.off[1] = (uint32_t)(lane >> 3) * row_bytes;
         return 0;
       },
-      [&](int64_t i, int c, u32x4 (&xs)[1][NS][S::XR]) {
+      [&](int i, int c, u32x4 (&xs)[1][NS][S::XR]) {
         if (nchunk == 1 && i > i0) return;   // the same for every unit
         const int t = lane & 15;
 #pragma unroll
@@ -283,16 +283,20 @@ __global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(FewArgs a) {
             if (t < a.T && k < a.d)
               xs[0][s][q] = *reinterpret_cast<const u32x4*>((const XT*)a.x + (int64_t)t * a.d + k);
           }
+        landed();
       },
-      [&](int64_t i, int g, int m, int n, float v) {
-        const int u = (int)(i / upe), f = (int)(i % upe) * (8 * NG) + 8 * g + (n & 7);
-        if (sizeof(WT) == 1)
-          v *= (n < 8 ? a.w.s_gate : a.w.s_up)[(int64_t)r.expert[u] * a.F + f];
+      [&](int i, int m, int n, float v) {
+        const int u = i / upe, f = i % upe * 8;
+        if constexpr (sizeof(WT) == 1) {
+          const int64_t row = (int64_t)r.expert[u] * a.F + f;
+          const float sg = pick<8>(a.w.s_gate, row, n & 7), su = pick<8>(a.w.s_up, row, n & 7);
+          v *= n < 8 ? sg : su;
+        }
         const float up = __shfl_xor(v, 8, 64);
         const uint32_t mask = r.mask[u];
         if (n < 8 && ((mask >> m) & 1u)) {
           const float h = v / (1.0f + expf(-v)) * up;
-          const int64_t o = (int64_t)(r.row0[u] + __popc(mask & ((1u << m) - 1))) * a.F + f;
+          const int64_t o = (int64_t)(r.row0[u] + __popc(mask & ((1u << m) - 1))) * a.F + f + n;
           if constexpr (sizeof(XT) == 4) {
             ((float*)a.H)[o] = h;
           } else {
@@ -304,42 +308,39 @@ __global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(FewArgs a) {
       });
 }
 
-// Partial down products: a unit is NG x 16 rows of W_down of an expert over one chunk of F
-// (NS steps per wave); the token operand (the expert's rows of h, in bf16 layers value and
-// remainder) stays in registers over the units of an (expert, chunk).
-template <typename WT, int NS, int NG>
+// Partial down products: a unit is 16 rows of W_down of an expert over one chunk of F (NS steps
+// per wave); the token operand (the expert's rows of h, in bf16 layers value and remainder)
+// stays in registers over the units of an (expert, chunk).
+template <typename WT, int NS, int R>
 __global__ __launch_bounds__(kFewThreads) void few_down_kernel(FewArgs a) {
   typedef Stream<WT> S;
   typedef typename S::X XT;
   constexpr int NH = sizeof(XT) == 4 ? 1 : 2;   // value, remainder
   __shared__ FewRoute r;
-  __shared__ StreamLds<NG> lds;
+  __shared__ StreamLds<R> lds;
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
   for (int i = tid; i < (int)(sizeof(FewRoute) / 4); i += kFewThreads)
     ((int*)&r)[i] = ((const int*)a.route)[i];
   __syncthreads();
-  const int upc = a.d / (16 * NG);   // units per (expert, chunk)
-  int64_t i0, i1, have = -1;
+  const int upc = a.d / 16;   // units per (expert, chunk)
+  int i0, i1, have = -1;
   share_of((int64_t)r.nu * a.chunks * upc, blockIdx.x, gridDim.x, i0, i1);
   const int nst = (a.F + S::SK - 1) / S::SK, row_bytes = a.F * (int)sizeof(WT);
-  stream_units<WT, NS, NS, NG, NH>(
+  stream_units<WT, NS, R, NH>(
       i0, i1, 1, nst, row_bytes, lds,
-      [&](int64_t i, const char* (&base)[NG][2]) {
-        const int64_t uc = i / upc;
-        const int64_t n0 =
-            (int64_t)r.expert[uc / a.chunks] * a.d + (i % upc) * (16 * NG) + (lane >> 3);
-#pragma unroll
-        for (int g = 0; g < NG; ++g)
-#pragma unroll
-          for (int q = 0; q < 2; ++q)
-            base[g][q] = (const char*)a.w.down + (n0 + 16 * g + 8 * q) * row_bytes;
-        return (int)(uc % a.chunks) * NS * kFewWaves;
+      [&](int i, UnitRows& rows) {
+        const int uc = i / upc;
+        const int64_t n0 = (int64_t)r.expert[uc / a.chunks] * a.d + i % upc * 16;
+        rows.base[0] = uniform((const char*)a.w.down + n0 * row_bytes);
+        rows.base[1] = rows.base[0] + 8 * (int64_t)row_bytes;
+        rows.off[0] = rows.off[1] = (uint32_t)(lane >> 3) * row_bytes;
+        return uc % a.chunks * NS * kFewWaves;
       },
-      [&](int64_t i, int, u32x4 (&xs)[NH][NS][S::XR]) {
-        const int64_t uc = i / upc;
+      [&](int i, int, u32x4 (&xs)[NH][NS][S::XR]) {
+        const int uc = i / upc;
         if (uc == have) return;
         have = uc;
-        const int u = (int)(uc / a.chunks), c = (int)(uc % a.chunks), t = lane & 15;
+        const int u = uc / a.chunks, c = uc % a.chunks, t = lane & 15;
         const uint32_t mask = r.mask[u];
         const bool mine = (mask >> t) & 1u;
         const int64_t o = (int64_t)(r.row0[u] + __popc(mask & ((1u << t) - 1))) * a.F;
@@ -356,15 +357,16 @@ __global__ __launch_bounds__(kFewThreads) void few_down_kernel(FewArgs a) {
                     (h == 0 ? (const XT*)a.H : (const XT*)a.Hlo) + o + k);
             }
           }
+        landed();
       },
-      [&](int64_t i, int g, int m, int q, float v) {
-        const int64_t uc = i / upc;
-        const int u = (int)(uc / a.chunks), n = (int)(i % upc) * (16 * NG) + 16 * g + q;
+      [&](int i, int m, int q, float v) {
+        const int uc = i / upc, u = uc / a.chunks, n0 = i % upc * 16;
         const uint32_t mask = r.mask[u];
+        if constexpr (sizeof(WT) == 1)
+          v *= pick<16>(a.w.s_down, (int64_t)r.expert[u] * a.d + n0, q);
         if (!((mask >> m) & 1u)) return;
-        if (sizeof(WT) == 1) v *= a.w.s_down[(int64_t)r.expert[u] * a.d + n];
         const int64_t row = r.row0[u] + __popc(mask & ((1u << m) - 1));
-        a.part[(row * a.chunks + uc % a.chunks) * a.d + n] = v;
+        a.part[(row * a.chunks + uc % a.chunks) * a.d + n0 + q] = v;
       });
 }
 
@@ -439,9 +441,9 @@ static moe_status_t validate_few(const moe_desc_t* d) {
   return d->T > kFew ? MOE_E_UNSUPPORTED : MOE_OK;
 }
 
-template <typename WT, int NS, int R, int NG>
+template <typename WT, int NS, int R>
 static void launch_gate_up_few(const FewArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL((few_gate_up_kernel<WT, NS, R, NG>), dim3(device_cu_count()), dim3(kFewThreads),
+  hipLaunchKernelGGL((few_gate_up_kernel<WT, NS, R>), dim3(device_cu_count()), dim3(kFewThreads),
                      0, s, a);
 }
 
@@ -451,29 +453,18 @@ static hipError_t launch_few(const FewArgs& a, hipStream_t s) {
   const int per = (int)ceil_div(ceil_div(a.d, Stream<WT>::SK), kFewWaves);   // steps per wave
   hipLaunchKernelGGL(few_logits_kernel<XT>, dim3((unsigned)ceil_div(a.E, 16), a.ks), dim3(kFewThreads),
                      0, s, a);
-  if constexpr (sizeof(WT) == 1) {
-    if (per <= 1)
-      launch_gate_up_few<WT, 1, 1, 2>(a, s);
-    else if (per <= 2)
-      launch_gate_up_few<WT, 2, 2, 2>(a, s);
-    else if (per <= 4)
-      launch_gate_up_few<WT, 4, 4, 2>(a, s);
-    else
-      launch_gate_up_few<WT, 8, 4, 1>(a, s);
-    hipLaunchKernelGGL((few_down_kernel<WT, kDownSteps / 2, 2>), dim3(device_cu_count()),
-                       dim3(kFewThreads), 0, s, a);
-  } else {
-    if (per <= 2)
-      launch_gate_up_few<WT, 2, 2, 1>(a, s);
-    else if (per <= 4)
-      launch_gate_up_few<WT, 4, 4, 1>(a, s);
-    else if (per <= 8)
-      launch_gate_up_few<WT, 8, 8, 1>(a, s);
-    else
-      launch_gate_up_few<WT, 14, 7, 1>(a, s);
-    hipLaunchKernelGGL((few_down_kernel<WT, kDownSteps, 1>), dim3(device_cu_count()),
-                       dim3(kFewThreads), 0, s, a);
-  }
+  if (per <= 2)
+    launch_gate_up_few<WT, 2, 8>(a, s);
+  else if (per <= 4)
+    launch_gate_up_few<WT, 4, 8>(a, s);
+  else if (per <= 8)
+    launch_gate_up_few<WT, 8, 8>(a, s);
+  else if constexpr (sizeof(WT) != 1)
+    launch_gate_up_few<WT, 14, 7>(a, s);
+  else
+    launch_gate_up_few<WT, 8, 8>(a, s);
+  hipLaunchKernelGGL((few_down_kernel<WT, sizeof(WT) == 1 ? kDownSteps / 2 : kDownSteps, 8>),
+                     dim3(device_cu_count()), dim3(kFewThreads), 0, s, a);
   hipLaunchKernelGGL(few_join_kernel<OT>, dim3((unsigned)ceil_div((int64_t)a.T * a.d, 256)),
                      dim3(256), 0, s, a);
   return hipGetLastError();

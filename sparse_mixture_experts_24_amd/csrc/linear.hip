@@ -52,11 +52,13 @@ __device__ __forceinline__ void act8(float* z, int act) {
   }
 }
 
-__device__ inline float scaled(float v, const float* scale, int n) {
-  return scale ? v * scale[n] : v;
-}
-__device__ inline float biased(float v, const float* bias, int n) {
-  return bias ? v + bias[n] : v;
+// p[n0 + q], 0 <= q < C, the last of n where that is past it.
+template <int C>
+__device__ __forceinline__ float column(const float* p, int n0, int n, int q) {
+  float v = scalar_f(p, n0);
+#pragma unroll
+  for (int j = 1; j < C; ++j) v = q == j ? scalar_f(p, min(n0 + j, n - 1)) : v;
+  return v;
 }
 __device__ inline float load_out(const LinearArgs& a, const void* base, int64_t i) {
   return a.out_f32 ? ((const float*)base)[i] : bf16_to_f32(((const bf16_t*)base)[i]);
@@ -112,32 +114,31 @@ __device__ __forceinline__ void store8(const LinearArgs& a, int64_t i, const flo
 }
 
 // ------------------------------------------------------------------ at most 16 rows
-// A unit is NG x 16 weight rows (gated: NG x 8 gate rows and the 8 matching up rows).
-template <typename WT, int NS, int R, int NG, bool GATED>
+// A unit is 16 weight rows (gated: 8 gate rows and the 8 matching up rows).
+template <typename WT, int NS, int R, bool GATED>
 __global__ __launch_bounds__(kStreamThreads) void linear_rows_kernel(LinearArgs a) {
   typedef Stream<WT> S;
   typedef typename S::X XT;
-  __shared__ StreamLds<NG> lds;
-  constexpr int COLS = GATED ? 8 : 16;   // output columns of a group
+  __shared__ StreamLds<R> lds;
+  constexpr int COLS = GATED ? 8 : 16;   // output columns of a unit
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-  int64_t i0, i1;
-  share_of((a.N + COLS * NG - 1) / (COLS * NG), blockIdx.x, gridDim.x, i0, i1);
+  int i0, i1;
+  share_of((a.N + COLS - 1) / COLS, blockIdx.x, gridDim.x, i0, i1);
   const int nst = (a.K + S::SK - 1) / S::SK;
   const int nchunk = (nst + NS * kStreamWaves - 1) / (NS * kStreamWaves);
-  stream_units<WT, NS, R, NG, 1>(
+  const uint32_t wrow = (uint32_t)(a.ldw * (int)sizeof(WT));
+  stream_units<WT, NS, R, 1>(
       i0, i1, nchunk, nst, a.K * (int)sizeof(WT), lds,
-      [&](int64_t i, const char* (&base)[NG][2]) {
+      [&](int i, UnitRows& rows) {
 #pragma unroll
-        for (int g = 0; g < NG; ++g)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int n = (int)i * COLS * NG + COLS * g + (GATED ? 0 : 8 * h) + (lane >> 3);
-            base[g][h] = (const char*)a.W[GATED ? h : 0] +
-                         min(n, a.N - 1) * a.ldw * (int)sizeof(WT);
-          }
+        for (int h = 0; h < 2; ++h) {
+          const int n0 = i * COLS, r = (GATED ? 0 : 8 * h) + (lane >> 3);
+          rows.base[h] = uniform((const char*)a.W[GATED ? h : 0] + n0 * (int64_t)wrow);
+          rows.off[h] = (uint32_t)min(r, a.N - 1 - n0) * wrow;
+        }
         return 0;
       },
-      [&](int64_t i, int c, u32x4 (&xs)[1][NS][S::XR]) {
+      [&](int i, int c, u32x4 (&xs)[1][NS][S::XR]) {
         if (nchunk == 1 && i > i0) return;   // the same for every unit
         const int t = lane & 15;
 #pragma unroll
@@ -149,17 +150,24 @@ __global__ __launch_bounds__(kStreamThreads) void linear_rows_kernel(LinearArgs 
             if (t < a.M && k < a.K)
               xs[0][s][q] = *reinterpret_cast<const u32x4*>((const XT*)a.x + t * a.ldx + k);
           }
+        landed();
       },
-      [&](int64_t i, int g, int m, int q, float v) {
-        const int n = (int)i * COLS * NG + COLS * g + (GATED ? q & 7 : q);
-        const int nc = min(n, a.N - 1), mat = GATED ? q >> 3 : 0;
-        v = biased(scaled(v, a.scale[mat], nc), a.bias[mat], nc);
+      [&](int i, int m, int q, float v) {
+        const int n0 = i * COLS, n = n0 + (GATED ? q & 7 : q);
+        // scale and bias by scalar loads, columns past N reading column N - 1
+        float z[GATED ? 2 : 1];
+#pragma unroll
+        for (int t = 0; t < (GATED ? 2 : 1); ++t) {
+          z[t] = v;
+          if (a.scale[t]) z[t] *= column<COLS>(a.scale[t], n0, a.N, q & (COLS - 1));
+          if (a.bias[t]) z[t] += column<COLS>(a.bias[t], n0, a.N, q & (COLS - 1));
+        }
         if constexpr (GATED) {
-          const float up = __shfl_xor(v, 8, 64);
-          v = act_f(v, a.act) * up;
+          const float up = __shfl_xor(z[1], 8, 64);
+          v = act_f(z[0], a.act) * up;
           if (q >= 8) return;
         } else {
-          v = act_f(v, a.act);
+          v = act_f(z[0], a.act);
         }
         if (m >= a.M || n >= a.N) return;
         if (a.residual) v += load_out(a, a.residual, m * a.ldr + n);
@@ -184,19 +192,6 @@ __global__ __launch_bounds__(kStreamThreads) void linear_rows_kernel(LinearArgs 
 // rows then cover 256 bytes, all 64 banks.
 //   Gated: the weight blocks of a wave alternate gate and up rows of the same columns, so
 // act(g) * u is formed in registers.
-// 16 bytes per lane from base + off straight into LDS at lds + 16 lane (base and lds, a byte
-// offset, are uniform).  The compiler does not count this load: wait with wait_loads()
-// before the barrier after which the data is read.
-__device__ __forceinline__ void load_to_lds(const char* base, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
-               :: "v"(off), "s"(base), "s"(lds));   // nothing else here uses m0
-}
-// All but the youngest N of the wave's loads to LDS have landed, every LDS read of this wave is
-// done, LDS contents are new to the compiler.
-template <int N = 0>
-__device__ __forceinline__ void wait_loads() {
-  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
-}
 // Barrier that LDS accesses do not cross.
 __device__ __forceinline__ void stage_barrier() {
   __builtin_amdgcn_s_barrier();
@@ -576,10 +571,10 @@ static hipError_t run_tiles(const LinearArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <typename WT, int NS, int R, int NG, bool GATED>
+template <typename WT, int NS, int R, bool GATED>
 static hipError_t run_rows(const LinearArgs& a, hipStream_t s) {
-  const int64_t units = ceil_div(a.N, (GATED ? 8 : 16) * NG);
-  hipLaunchKernelGGL((linear_rows_kernel<WT, NS, R, NG, GATED>),
+  const int64_t units = ceil_div(a.N, GATED ? 8 : 16);
+  hipLaunchKernelGGL((linear_rows_kernel<WT, NS, R, GATED>),
                      dim3((unsigned)std::min<int64_t>(units, device_cu_count())),
                      dim3(kStreamThreads), 0, s, a);
   return hipGetLastError();
@@ -590,17 +585,12 @@ static hipError_t run_rows(const LinearArgs& a, hipStream_t s) {
 template <typename WT, bool GATED>
 static hipError_t launch_rows(const LinearArgs& a, hipStream_t s) {
   const int64_t per = ceil_div(ceil_div(a.K, Stream<WT>::SK), kStreamWaves);
-  if constexpr (sizeof(WT) == 1) {
-    if (per <= 1) return run_rows<WT, 1, 1, 2, GATED>(a, s);
-    if (per <= 2) return run_rows<WT, 2, 2, 2, GATED>(a, s);
-    if (per <= 4) return run_rows<WT, 4, 4, 2, GATED>(a, s);
-    return run_rows<WT, 8, 4, 1, GATED>(a, s);
-  } else {
-    if (per <= 2) return run_rows<WT, 2, 2, 1, GATED>(a, s);
-    if (per <= 4) return run_rows<WT, 4, 4, 1, GATED>(a, s);
-    if (per <= 8) return run_rows<WT, 8, 8, 1, GATED>(a, s);
-    return run_rows<WT, 14, 7, 1, GATED>(a, s);
+  if (per <= 2) return run_rows<WT, 2, 8, GATED>(a, s);
+  if (per <= 4) return run_rows<WT, 4, 8, GATED>(a, s);
+  if constexpr (sizeof(WT) != 1) {   // an 8-bit step takes twice the token operand
+    if (per > 8) return run_rows<WT, 14, 7, GATED>(a, s);
   }
+  return run_rows<WT, 8, 8, GATED>(a, s);
 }
 
 template <typename WT, bool GATED>

@@ -9,9 +9,9 @@
 // A step is 128 bytes of each of the 16 rows (SK elements); wave w takes steps w, w + 8, ...
 // so the workgroup reads 1 KB runs of a row.  A step is loaded with 8 lanes per 128-byte
 // segment (a lane per row, as the MFMA operand has it, would run the load path at a quarter
-// of its rate) and put into operand order through a wave-private LDS buffer: 16-byte chunk
-// c of row r at position c ^ ((r / 2) % 8), conflict-free both ways.  Lane (row r, group g)
-// then holds chunks 2 g and 2 g + 1 of its row; token operands use the same k order.
+// of its rate) and comes into operand order through wave-private LDS: 16-byte chunk c of row
+// r at position c ^ ((r / 2) % 8), conflict-free both ways.  Lane (row r, group g) then holds
+// chunks 2 g and 2 g + 1 of its row; token operands use the same k order.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -159,103 +159,171 @@ __device__ __forceinline__ float red_get(const float* red, int red_stride, int m
 }
 
 // Share s of `of`: a run of consecutive units of n, the shares as even as they go.
-__device__ inline void share_of(int64_t n, int s, int of, int64_t& i0, int64_t& i1) {
-  i0 = n * s / of;
-  i1 = n * (s + 1) / of;
+__device__ inline void share_of(int64_t n, int s, int of, int& i0, int& i1) {
+  i0 = (int)(n * s / of);
+  i1 = (int)(n * (s + 1) / of);
 }
 
-// LDS of stream_units.
-template <int NG>
+// LDS of stream_units: the waves' rings of steps, the waves' sums of a unit (two, in turn).
+template <int R>
 struct StreamLds {
-  __align__(16) char stage[kStreamWaves][kStageBytes];
-  float red[2][kStreamWaves * NG * kRedWave];
+  __align__(16) char ring[kStreamWaves][R][kStageBytes];
+  float red[2][kStreamWaves * kRedWave];
 };
 
-// Units i0 .. i1 - 1 of NG x 16 weight rows each, against a token operand that stays in
-// registers while it can.  A unit is visited once per chunk of NS steps per wave (NS x 8
-// steps of the row; one chunk where the row is no longer).  A ring of R steps (R divides
-// NS) runs across the visits: as step s is used, step s + R goes out, of this visit or of
-// the next, so a wave always has R NG 2 KB in flight.
-//   point(i, base)       base[g][h]: the lane's row of load h of group g; returns the row's
-//                        first step
+// 16 bytes per lane from base + off straight into LDS at lds + 16 lane (base and lds, a byte
+// offset, are uniform).  The compiler does not count this load: wait with wait_loads().
+__device__ __forceinline__ void load_to_lds(const char* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+               :: "v"(off), "s"(base), "s"(lds));   // nothing else here uses m0
+}
+// All but the youngest N of the wave's memory operations have landed, every LDS access of this
+// wave is done, LDS contents are new to the compiler.
+template <int N = 0>
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+}
+// Every vector load of the wave has landed, said so that the compiler knows it: a load whose
+// value lives across visits would otherwise be waited for, and the ring with it, at its
+// first use in every visit.
+__device__ __forceinline__ void landed() {
+  __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0), the other counters free
+}
+// LDS byte offset of p, for load_to_lds.
+__device__ __forceinline__ uint32_t lds_offset(const void* p) {
+  return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(
+      const __attribute__((address_space(3))) char*)p);
+}
+// A pointer that is the same in the whole wave, in scalar registers.
+__device__ __forceinline__ const char* uniform(const char* p) {
+  const uint64_t v = (uint64_t)p;
+  return (const char*)((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32 |
+                       (uint32_t)__builtin_amdgcn_readfirstlane((int)v));
+}
+
+// p[i] through the scalar cache, for values that no kernel writes and an index that is the
+// same in the whole wave: a vector load's wait would also wait for the loads to LDS.
+__device__ __forceinline__ float scalar_f(const float* p, int64_t i) {
+  return *(const __attribute__((address_space(4))) float*)uniform((const char*)(p + i));
+}
+
+// p[i + q], 0 <= q < N: N scalar loads and a choice per lane.
+template <int N>
+__device__ __forceinline__ float pick(const float* p, int64_t i, int q) {
+  const auto* s = (const __attribute__((address_space(4))) float*)uniform((const char*)(p + i));
+  float v = s[0];
+#pragma unroll
+  for (int j = 1; j < N; ++j) v = q == j ? s[j] : v;
+  return v;
+}
+// Where the rows of a unit are: load h takes row h * 8 + lane / 8 at base[h] + off[h].
+struct UnitRows {
+  const char* base[2];   // uniform
+  uint32_t off[2];       // per lane
+};
+
+// Units i0 .. i1 - 1 of 16 weight rows each, against a token operand that stays in registers
+// while it can.  A unit is visited once per chunk of NS steps per wave (NS x 8 steps of the
+// row; one chunk where the row is no longer).  The steps come through a ring of R in LDS,
+// filled by direct loads: as a step is used, the one R further goes out, of this visit or a
+// later one (R divides NS or NS divides R), so a wave always has R x 2 KB in flight and no
+// registers wait for them.
+//   point(i, rows)       where unit i is; returns the row's first step
 //   load_x(i, c, xs)     the wave's token operand of chunk c, xs[0 .. NH - 1] multiplied by
-//                        the same weights (only called where it may have changed)
-//   done(i, g, m, n, v)  sum v of token m and row n of group g, called by 256 threads (whole
-//                        waves) for each group; ends the unit
+//                        the same weights (may leave it as it is); ends with landed()
+//   done(i, m, n, v)     sum v of token m and weight row n of the unit, called by 256 threads
+//                        (whole waves); a vector load there empties the ring
 //   nst, row_bytes       steps and bytes of a weight row
 // Steps past nst repeat its last one and bytes past the row its last chunk (cache hits); the
 // token operand must be zero there.
-template <typename WT, int NS, int R, int NG, int NH, typename Point, typename LoadX,
-          typename Done>
-__device__ __forceinline__ void stream_units(int64_t i0, int64_t i1, int nchunk, int nst,
-                                             int row_bytes, StreamLds<NG>& lds, Point point,
-                                             LoadX load_x, Done done) {
+template <typename WT, int NS, int R, int NH, typename Point, typename LoadX, typename Done>
+__device__ __forceinline__ void stream_units(int i0, int i1, int nchunk, int nst, int row_bytes,
+                                             StreamLds<R>& lds, Point point, LoadX load_x,
+                                             Done done) {
   typedef Stream<WT> S;
-  static_assert(NS % R == 0, "ring slots keep their steps");
+  static_assert(NS % R == 0 || R % NS == 0, "the ring's phase is the same in every visit");
+  constexpr int AHEAD = R >= NS ? R / NS : 1;   // visits from a step's use to the one loaded
+  i0 = __builtin_amdgcn_readfirstlane(i0);   // the same in every lane, in scalar registers
+  i1 = __builtin_amdgcn_readfirstlane(i1);
   if (i0 >= i1) return;
-  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
-  char* stage = lds.stage[wv];
-  u32x4 xs[NH][NS][S::XR], ring[R][NG][2];
-  const char* base[NG][2];
-  auto load = [&](int s, int st0) {
-    const int st = min(st0 + s * kStreamWaves + wv, nst - 1);
-    const int byte = min(st * kStepBytes + 16 * (lane & 7), row_bytes - 16);
-#pragma unroll
-    for (int g = 0; g < NG; ++g)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        ring[s % R][g][h] = *reinterpret_cast<const u32x4*>(base[g][h] + byte);
+  const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int visits = (i1 - i0) * nchunk;
+  const uint32_t ring = lds_offset(lds.ring[wv][0]);
+  u32x4 xs[NH][NS][S::XR];
+  UnitRows rows;
+  int first = 0;   // first step of the visit that rows points to
+  auto point_at = [&](int v) {
+    first = point(i0 + v / nchunk, rows) + v % nchunk * NS * kStreamWaves;
   };
-  floatx4 acc[NG];
-  int first = point(i0, base);   // of the unit that base points to
-  // Chunk c of a unit; in, cn: the next visit, if there is one.
-  auto visit = [&](auto more, int c, int64_t in, int cn) {
-    const int st0 = first + c * NS * kStreamWaves;
-    int stn = 0;
+  // A load of 8 rows: chunk c of row r goes to position c ^ (r / 2 % 8).
+  auto load = [&](int s, uint32_t slot) {
+    const int st = min(first + s * kStreamWaves + wv, nst - 1);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int chunk = (lane & 7) ^ (4 * h | (lane >> 4));
+      const int byte = min(st * kStepBytes + 16 * chunk, row_bytes - 16);
+      load_to_lds(rows.base[h], rows.off[h] + (uint32_t)byte, ring + slot + h * (kStageBytes / 2));
+    }
+  };
+  floatx4 acc;
+  uint32_t slot = 0;   // of the step in use, bytes from ring
+  // Visit v; more: the steps R further exist for all of its steps.
+  auto visit = [&](auto more, int v) {
+    if (AHEAD > 1 || R == NS) {
+      if constexpr (decltype(more)::value) point_at(v + AHEAD);
+    }
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
-#pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        u32x4 w0, w1;
-        stage_in(stage, lane, ring[s % R][g][0], ring[s % R][g][1]);
-        stage_out(stage, lane, w0, w1);
-#pragma unroll
-        for (int h = 0; h < NH; ++h) S::mma(acc[g], xs[h][s], w0, w1);
+      // steps that may still be under way when this one is needed
+      constexpr int rest_max = R - 1;
+      const int rest = decltype(more)::value ? rest_max : (NS - 1 - s < rest_max ? NS - 1 - s : rest_max);
+      switch (rest) {   // a constant once unrolled
+#define MOE_WAIT(n) case n: wait_loads<2 * n>(); break;
+        MOE_WAIT(0) MOE_WAIT(1) MOE_WAIT(2) MOE_WAIT(3) MOE_WAIT(4) MOE_WAIT(5) MOE_WAIT(6)
+#undef MOE_WAIT
+        default: wait_loads<14>(); break;
       }
+      u32x4 w0, w1;
+      stage_out(lds.ring[wv][0] + slot, lane, w0, w1);
+      // the slot is read out before it is filled again
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
       if (s + R < NS) {
-        load(s + R, st0);
+        load(s + R, slot);
       } else if constexpr (decltype(more)::value) {
-        if (s + R == NS) {
-          first = point(in, base);
-          stn = first + cn * NS * kStreamWaves;
-        }
-        load(s + R - NS, stn);
+        if (R < NS && s + R == NS) point_at(v + 1);
+        load(R < NS ? s + R - NS : s, slot);
       }
-      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int h = 0; h < NH; ++h) S::mma(acc, xs[h][s], w0, w1);
+      slot = __builtin_amdgcn_readfirstlane(slot == (R - 1) * kStageBytes ? 0 : slot + kStageBytes);
     }
   };
+  static_assert(R <= 8, "waits");
 #pragma unroll
-  for (int s = 0; s < R; ++s) load(s, first);
-  int par = 0;
-  for (int64_t i = i0; i < i1; ++i) {
+  for (int q = 0; q < AHEAD; ++q)
+    if (q < visits) {
+      point_at(q);
 #pragma unroll
-    for (int g = 0; g < NG; ++g) acc[g] = floatx4{0.f, 0.f, 0.f, 0.f};
-    for (int c = 0; c < nchunk; ++c) {
-      load_x(i, c, xs);
-      const bool last = c + 1 == nchunk;
-      if (last && i + 1 == i1)
-        visit(std::false_type{}, c, 0, 0);
-      else
-        visit(std::true_type{}, c, last ? i + 1 : i, last ? 0 : c + 1);
+      for (int s = 0; s < (R < NS ? R : NS); ++s) load(s, (q * NS + s) * kStageBytes);
     }
-#pragma unroll
-    for (int g = 0; g < NG; ++g) red_put(lds.red[par] + (wv * NG + g) * kRedWave, acc[g]);
+  int par = 0;
+  for (int v = 0, i = i0; i < i1; ++i) {
+    acc = floatx4{0.f, 0.f, 0.f, 0.f};
+    for (int c = 0; c < nchunk; ++c, ++v) {
+      load_x(i, c, xs);
+      if (v + AHEAD < visits)
+        visit(std::true_type{}, v);
+      else
+        visit(std::false_type{}, v);
+    }
+    red_put(lds.red[par] + wv * kRedWave, acc);
     __syncthreads();
-    // one half of the workgroup (NG 1: the halves take turns; NG 2: one group each) sums up;
-    // the other buffer is free until it has passed the next barrier
-    const int half = tid >> 8, g = NG == 1 ? 0 : half, m = (tid >> 4) & 15, n = tid & 15;
-    if (NG == 2 || half == par)
-      done(i, g, m, n, red_get(lds.red[par] + g * kRedWave, NG * kRedWave, m, n));
+    // the halves of the workgroup take turns to sum up; the other buffer is free until the
+    // summing half has passed the next barrier
+    if (tid >> 8 == par) {
+      const int m = (tid >> 4) & 15, n = tid & 15;
+      done(i, m, n, red_get(lds.red[par], kRedWave, m, n));
+    }
     par ^= 1;
   }
 }
