@@ -18,6 +18,9 @@
 namespace moe {
 
 constexpr int kFew = MOE_FEW_TOKENS;
+// Experts of a router whose logits every workgroup of the gate/up kernel computes for itself (one
+// MFMA block; reading the router again from each L2 costs less than a launch).
+constexpr int kOwnLogits = 16;
 constexpr int kFewThreads = kStreamThreads, kFewWaves = kStreamWaves;
 
 struct FewRoute;
@@ -31,7 +34,7 @@ struct FewArgs {
   void* out;
   float* f;
   float* p;
-  float* logits;     // [ks, T, E] partial sums
+  float* logits;     // [ks, T, E] partial sums, or NULL (every workgroup's own)
   FewRoute* route;   // the routing, for the kernels after the first expert kernel
   void* H;           // [T*k + S*T, F] expert-contiguous rows: float, or bf16 values
   bf16_t* Hlo;       //   and (bf16 layers) the bf16 remainders
@@ -39,6 +42,7 @@ struct FewArgs {
   int T, d, E, F, k, S, C;   // C: capacity, -1 none
   int ks;            // parts that the logits are summed in
   int chunks;        // parts that the down products' F range is summed in
+  bool out_f32;
 };
 
 // The routing of the call, held by every workgroup.
@@ -52,12 +56,6 @@ struct FewRoute {
 };
 static_assert(sizeof(FewRoute) % 4 == 0, "copied as int32");
 
-__device__ inline float wide(const float* p) { return *p; }
-__device__ inline float wide(const bf16_t* p) { return bf16_to_f32(*p); }
-__device__ inline float wide(const uint8_t* p) { return __builtin_amdgcn_cvt_f32_fp8((int)*p, 0); }
-__device__ inline void narrow(float* p, float v) { *p = v; }
-__device__ inline void narrow(bf16_t* p, float v) { *p = f32_to_bf16(v); }
-
 // What the routing needs of LDS while it is formed.
 struct RouteLds {
   uint32_t chosen[kMaxExperts];   // token set of each expert
@@ -67,7 +65,8 @@ struct RouteLds {
 
 // Softmax and top-k of the wave's tokens, at most NV experts per lane.
 template <int NV>
-__device__ __forceinline__ void route_tokens(const FewArgs& a, FewRoute& r, RouteLds& l) {
+__device__ __forceinline__ void route_tokens(const FewArgs& a, FewRoute& r, RouteLds& l,
+                                             const float* logits) {
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
   float bias[NV], ps[NV] = {};
 #pragma unroll
@@ -80,7 +79,7 @@ __device__ __forceinline__ void route_tokens(const FewArgs& a, FewRoute& r, Rout
     for (int q = 0; q < a.ks; ++q)   // the logits' partial sums, in order
 #pragma unroll
       for (int i = 0; i < NV; ++i)
-        if (lane + 64 * i < a.E) v[i] += a.logits[(q * a.T + t) * a.E + lane + 64 * i];
+        if (lane + 64 * i < a.E) v[i] += logits[(q * a.T + t) * a.E + lane + 64 * i];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       if (lane + 64 * i >= a.E) v[i] = -INFINITY;
@@ -134,18 +133,18 @@ __device__ __forceinline__ void route_tokens(const FewArgs& a, FewRoute& r, Rout
 
 // Softmax, top-k, capacity and the touched experts from the logits, by one workgroup.
 // Block 0 also writes f and P.  Ends with a barrier.
-__device__ inline void few_route(const FewArgs& a, FewRoute& r, RouteLds& l) {
+__device__ inline void few_route(const FewArgs& a, FewRoute& r, RouteLds& l, const float* logits) {
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
   const int nv = (a.E + 63) / 64;
   uint32_t* chosen = l.chosen;
   for (int e = tid; e < 64 * nv; e += kFewThreads) chosen[e] = 0;
   __syncthreads();
   if (nv == 1)
-    route_tokens<1>(a, r, l);
+    route_tokens<1>(a, r, l, logits);
   else if (nv <= 4)
-    route_tokens<4>(a, r, l);
+    route_tokens<4>(a, r, l, logits);
   else
-    route_tokens<8>(a, r, l);
+    route_tokens<8>(a, r, l, logits);
   __syncthreads();
   if (blockIdx.x == 0) {
     for (int e = tid; e < a.E; e += kFewThreads) {
@@ -214,29 +213,38 @@ __device__ inline void few_route(const FewArgs& a, FewRoute& r, RouteLds& l) {
   __syncthreads();
 }
 
-// Router logits of 16 experts (blockIdx.x) over one part of d (blockIdx.y).
+// Router logits of experts e0 .. e0 + 15 over steps st0 .. st1 - 1 of d, into out[T][ld].  Ends
+// with the writes.
+struct LogitsLds {
+  __align__(16) char stage[kFewWaves][kStageBytes];
+  float red[kFewWaves * kRedWave];
+};
 template <typename XT>
-__global__ __launch_bounds__(kFewThreads) void few_logits_kernel(FewArgs a) {
-  __shared__ __align__(16) char stage[kFewWaves][kStageBytes];
-  __shared__ float red[kFewWaves * kRedWave];
-  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
-  const int e0 = blockIdx.x * 16, t = lane & 15;
+__device__ __forceinline__ void few_logits(const FewArgs& a, LogitsLds& l, int e0, int st0,
+                                           int st1, float* out) {
+  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, t = lane & 15;
   const XT* x = (const XT*)a.x + (int64_t)min(t, a.T - 1) * a.d;
   const char* row[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i)
     row[i] = (const char*)a.Wr +
              (int64_t)min(e0 + 8 * i + (lane >> 3), a.E - 1) * a.d * (int)sizeof(XT);
-  const int nst = a.d / Stream<XT>::SK;
-  const int st0 = nst * blockIdx.y / a.ks, st1 = nst * (blockIdx.y + 1) / a.ks;
   floatx4 acc = {0.f, 0.f, 0.f, 0.f};
-  stream_rows<XT, 4>(acc, stage[wv], st0, st1, [&](int i, int byte) { return row[i] + byte; },
+  stream_rows<XT, 4>(acc, l.stage[wv], st0, st1, [&](int i, int byte) { return row[i] + byte; },
                      [&](int k) { return t < a.T ? x + k : nullptr; });
-  red_put(red + wv * kRedWave, acc);
+  red_put(l.red + wv * kRedWave, acc);
   __syncthreads();
   const int m = tid >> 4, n = tid & 15;
-  if (m < a.T && e0 + n < a.E)
-    a.logits[((int)blockIdx.y * a.T + m) * a.E + e0 + n] = red_get(red, kRedWave, m, n);
+  if (m < a.T && e0 + n < a.E) out[m * a.E + e0 + n] = red_get(l.red, kRedWave, m, n);
+}
+
+// 16 experts (blockIdx.x) over one part of d (blockIdx.y).
+template <typename XT>
+__global__ __launch_bounds__(kFewThreads) void few_logits_kernel(FewArgs a) {
+  __shared__ LogitsLds l;
+  const int nst = a.d / Stream<XT>::SK, y = blockIdx.y;
+  few_logits<XT>(a, l, blockIdx.x * 16, nst * y / a.ks, nst * (y + 1) / a.ks,
+                 a.logits + y * a.T * a.E);
 }
 
 // h = SiLU(x W_gate^T) * (x W_up^T).  A unit is 8 gate rows and the 8 matching up rows of a
@@ -248,10 +256,20 @@ __global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(FewArgs a) {
   typedef typename S::X XT;
   __shared__ FewRoute r;
   __shared__ union {
-    RouteLds route;
+    struct {
+      LogitsLds logits;
+      float sums[kFew * kOwnLogits];
+      RouteLds route;
+    };
     StreamLds<R> stream;
   } lds;
-  few_route(a, r, lds.route);
+  if (a.logits) {
+    few_route(a, r, lds.route, a.logits);
+  } else {   // a small router: every workgroup computes the logits itself
+    few_logits<XT>(a, lds.logits, 0, 0, a.d / Stream<XT>::SK, lds.sums);
+    __syncthreads();
+    few_route(a, r, lds.route, lds.sums);
+  }
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
   if (blockIdx.x == 0)
     for (int i = tid; i < (int)(sizeof(FewRoute) / 4); i += kFewThreads)
@@ -370,24 +388,49 @@ __global__ __launch_bounds__(kFewThreads) void few_down_kernel(FewArgs a) {
       });
 }
 
-// y_t = sum over slots of w (sum over chunks), the shared expert, the residual.
-template <typename OT>
-__global__ __launch_bounds__(256) void few_join_kernel(FewArgs a) {
-  const FewRoute& r = *a.route;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+// y = sum over the slots of w (sum over chunks), the shared expert, the residual; a thread per
+// output, eight partial sums loaded at a time (what bounds it is their latency).
+constexpr int kJoinThreads = 256;
+__global__ __launch_bounds__(kJoinThreads) void few_join_kernel(FewArgs a) {
+  __shared__ FewRoute r;
+  for (int i = threadIdx.x; i < (int)(sizeof(FewRoute) / 4); i += kJoinThreads)
+    ((int*)&r)[i] = ((const int*)a.route)[i];
+  __syncthreads();
+  const int64_t i = (int64_t)blockIdx.x * kJoinThreads + threadIdx.x;
   if (i >= (int64_t)a.T * a.d) return;
   const int t = (int)(i / a.d), n = (int)(i % a.d);
-  float y = 0.0f;
-  for (int j = 0; j <= a.k; ++j) {
-    const int row = r.row[t][j];
-    if (row < 0) continue;
-    const float* p = a.part + (int64_t)row * a.chunks * a.d + n;
-    float s = 0.0f;
-    for (int c = 0; c < a.chunks; ++c) s += p[(int64_t)c * a.d];
-    y += j < a.k ? r.w[t][j] * s : s;
+  float y = 0.0f, s = 0.0f, res = 0.0f;
+  if (a.residual)
+    res = a.out_f32 ? ((const float*)a.residual)[i] : bf16_to_f32(((const bf16_t*)a.residual)[i]);
+  for (int j = 0, c = 0; j <= a.k;) {
+    float v[8];
+    int jj = j, cc = c;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const int row = jj <= a.k ? r.row[t][jj] : -1;
+      v[q] = row >= 0 ? a.part[((int64_t)row * a.chunks + cc) * a.d + n] : 0.0f;
+      if (++cc == a.chunks) {
+        cc = 0;
+        ++jj;
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      if (j > a.k) break;
+      s += v[q];
+      if (++c == a.chunks) {
+        if (r.row[t][j] >= 0) y += j < a.k ? r.w[t][j] * s : s;
+        s = 0.0f;
+        c = 0;
+        ++j;
+      }
+    }
   }
-  if (a.residual) y += wide((const OT*)a.residual + i);
-  narrow((OT*)a.out + i, y);
+  y += res;
+  if (a.out_f32)
+    ((float*)a.out)[i] = y;
+  else
+    ((bf16_t*)a.out)[i] = f32_to_bf16(y);
 }
 
 // ------------------------------------------------------------------ host
@@ -403,6 +446,7 @@ struct FewWorkspace {
 // Parts of d that the logits are summed in: one or two steps per wave each, as long as a
 // workgroup's routing reads at most 1024 partial sums per token.
 static int64_t logit_parts(const moe_desc_t& d) {
+  if (d.n_experts <= kOwnLogits) return 1;
   const int64_t steps = d.d_model / (d.dtype == MOE_DTYPE_F32 ? Stream<float>::SK : Stream<bf16_t>::SK);
   return std::min(ceil_div(steps, 2 * kFewWaves), std::max<int64_t>(1, 1024 / d.n_experts));
 }
@@ -447,12 +491,13 @@ static void launch_gate_up_few(const FewArgs& a, hipStream_t s) {
                      0, s, a);
 }
 
-template <typename WT, typename OT>
+template <typename WT>
 static hipError_t launch_few(const FewArgs& a, hipStream_t s) {
   typedef typename Stream<WT>::X XT;
   const int per = (int)ceil_div(ceil_div(a.d, Stream<WT>::SK), kFewWaves);   // steps per wave
-  hipLaunchKernelGGL(few_logits_kernel<XT>, dim3((unsigned)ceil_div(a.E, 16), a.ks), dim3(kFewThreads),
-                     0, s, a);
+  if (a.logits)
+    hipLaunchKernelGGL(few_logits_kernel<XT>, dim3((unsigned)ceil_div(a.E, 16), a.ks),
+                       dim3(kFewThreads), 0, s, a);
   if (per <= 2)
     launch_gate_up_few<WT, 2, 8>(a, s);
   else if (per <= 4)
@@ -465,8 +510,8 @@ static hipError_t launch_few(const FewArgs& a, hipStream_t s) {
     launch_gate_up_few<WT, 8, 8>(a, s);
   hipLaunchKernelGGL((few_down_kernel<WT, sizeof(WT) == 1 ? kDownSteps / 2 : kDownSteps, 8>),
                      dim3(device_cu_count()), dim3(kFewThreads), 0, s, a);
-  hipLaunchKernelGGL(few_join_kernel<OT>, dim3((unsigned)ceil_div((int64_t)a.T * a.d, 256)),
-                     dim3(256), 0, s, a);
+  hipLaunchKernelGGL(few_join_kernel, dim3((unsigned)ceil_div((int64_t)a.T * a.d, kJoinThreads)),
+                     dim3(kJoinThreads), 0, s, a);
   return hipGetLastError();
 }
 
@@ -508,7 +553,7 @@ static moe_status_t few_impl(const moe_desc_t* desc, const void* x, const void* 
                   out,
                   f,
                   p,
-                  w.logits,
+                  d.n_experts > kOwnLogits ? w.logits : nullptr,
                   w.route,
                   w.H,
                   w.Hlo,
@@ -521,15 +566,11 @@ static moe_status_t few_impl(const moe_desc_t* desc, const void* x, const void* 
                   (int)d.n_shared,
                   (int)capacity_of(d),
                   (int)logit_parts(d),
-                  (int)down_chunks(d, ew.fp8)};
-  const bool of32 = d.out_dtype == MOE_DTYPE_F32;
-  hipError_t e;
-  if (ew.fp8)
-    e = of32 ? launch_few<uint8_t, float>(a, s) : launch_few<uint8_t, bf16_t>(a, s);
-  else if (d.dtype == MOE_DTYPE_F32)
-    e = of32 ? launch_few<float, float>(a, s) : launch_few<float, bf16_t>(a, s);
-  else
-    e = of32 ? launch_few<bf16_t, float>(a, s) : launch_few<bf16_t, bf16_t>(a, s);
+                  (int)down_chunks(d, ew.fp8),
+                  d.out_dtype == MOE_DTYPE_F32};
+  const hipError_t e = ew.fp8                         ? launch_few<uint8_t>(a, s)
+                       : d.dtype == MOE_DTYPE_F32 ? launch_few<float>(a, s)
+                                                  : launch_few<bf16_t>(a, s);
   return e == hipSuccess ? MOE_OK : MOE_E_HIP;
 }
 
