@@ -26,13 +26,27 @@ struct LinearArgs {
   bool out_f32, wide_rows;
 };
 
-__device__ inline float act_f(float z, int act) {
+// The activations to some 3e-7 of |z| (exponential and reciprocal of the hardware).  GELU: the
+// complementary error function of x = |z| / sqrt 2 as t (a1 + .. + a5 t^4) exp(-x^2) with
+// t = 1 / (1 + p x) (Abramowitz and Stegun, 7.1.26, within 1.5e-7), a quarter of erff's
+// instructions; the tails keep the sign and never cancel.
+__device__ __forceinline__ float act_f(float z, int act) {
   switch (act) {
     case MOE_ACT_RELU: return fmaxf(z, 0.0f);
-    case MOE_ACT_GELU: return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
+    case MOE_ACT_GELU: {
+      const float x = fabsf(z) * 0.70710678118654752f;
+      const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f, x, 1.0f));
+      float p = fmaf(1.061405429f, t, -1.453152027f);
+      p = fmaf(p, t, 1.421413741f);
+      p = fmaf(p, t, -0.284496736f);
+      p = fmaf(p, t, 0.254829592f);
+      const float tail = 0.5f * z * (p * t) * __expf(-x * x);   // z/2 erfc(x)
+      return z >= 0.0f ? z - tail : tail;
+    }
     case MOE_ACT_GELU_TANH:
-      return z / (1.0f + expf(-1.5957691216057308f * (z + 0.044715f * z * z * z)));
-    case MOE_ACT_SILU: return z / (1.0f + expf(-z));
+      return z * __builtin_amdgcn_rcpf(
+                     1.0f + __expf(-1.5957691216057308f * fmaf(0.044715f * z * z, z, z)));
+    case MOE_ACT_SILU: return z * __builtin_amdgcn_rcpf(1.0f + __expf(-z));
     default: return z;
   }
 }
@@ -190,6 +204,8 @@ __global__ __launch_bounds__(kStreamThreads) void linear_rows_kernel(LinearArgs 
 // c ^ (r / 2 % 8) (8-bit: c ^ (r / 4 % 4)), applied to the addresses that the lanes load
 // from: a direct load puts lane l's 16 bytes at 16 l.  The operand reads of 16 neighbouring
 // rows then cover 256 bytes, all 64 banks.
+//   Small products have less than a tile for every CU: there WK groups of waves with stages of
+// their own take every WK-th step and their sums are added through LDS.
 //   Gated: the weight blocks of a wave alternate gate and up rows of the same columns, so
 // act(g) * u is formed in registers.
 // Barrier that LDS accesses do not cross.
@@ -259,10 +275,15 @@ constexpr bool tile_slots() {
   return ST == 2 && 2 * tile_m<MB, WM>() * kXRow == tile_stage_bytes<WT, MB, NB, WM, WN>();
 }
 template <typename WT, int MB, int NB, int WM, int WN, int ST>
-constexpr int tile_lds_bytes() {
+constexpr int tile_group_bytes() {
   const int stage = tile_stage_bytes<WT, MB, NB, WM, WN>();
-  const int stages = tile_slots<WT, MB, NB, WM, WN, ST>() ? 5 * stage / 2 : ST * stage;
-  const int epi = WM * WN * 32 * tile_epilogue_ld<NB>() * 4;
+  return tile_slots<WT, MB, NB, WM, WN, ST>() ? 5 * stage / 2 : ST * stage;
+}
+template <typename WT, int MB, int NB, int WM, int WN, int WK, int ST>
+constexpr int tile_lds_bytes() {
+  const int stages = WK * tile_group_bytes<WT, MB, NB, WM, WN, ST>();
+  const int sums = (WK - 1) * tile_m<MB, WM>() * tile_w<NB, WN>() * 4;
+  const int epi = sums + WM * WN * 32 * tile_epilogue_ld<NB>() * 4;
   return stages > epi ? stages : epi;
 }
 
@@ -277,8 +298,8 @@ __device__ inline void tile_of(const LinearArgs& a, int tiles_m, int tiles_n, in
   tn = pos % per / rows;
 }
 
-template <typename WT, int MB, int NB, int WM, int WN, int ST, bool GATED>
-__global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearArgs a) {
+template <typename WT, int MB, int NB, int WM, int WN, int WK, int ST, bool GATED>
+__global__ __launch_bounds__(64 * WM * WN * WK) void linear_tile_kernel(LinearArgs a) {
   typedef Tile<WT> TT;
   typedef typename TT::X XT;
   static_assert(!GATED || NB % 2 == 0, "gate and up blocks come in pairs");
@@ -292,7 +313,10 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearArgs a)
   static_assert(!GATED || NW * WRPL <= 64, "half of a wave's weight rows are of one matrix");
   extern __shared__ __align__(16) char smem[];
   const int tid = threadIdx.x, lane = tid & 63;
-  const int w = __builtin_amdgcn_readfirstlane(tid >> 6), wm = w / WN, wn = w % WN;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wk = wave / (WM * WN);
+  const int w = wave % (WM * WN), wm = w / WN, wn = w % WN;
+  constexpr int GROUP = tile_group_bytes<WT, MB, NB, WM, WN, ST>();
+  const int lds0 = wk * GROUP;   // the group's stages
   int tm, tn;
   tile_of(a, (a.M + BM - 1) / BM, (a.N + OUT_N - 1) / OUT_N, tm, tn);
   const int m0 = tm * BM, n0 = tn * OUT_N;
@@ -315,25 +339,27 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearArgs a)
     const int col = GATED ? (j / (32 * NB)) * (16 * NB) + ((j / 32) % NB >> 1) * 32 + (j & 31) : j;
     ow[i] = (uint32_t)(min(n0 + col, a.N - 1) - n0) * wrow + 16 * (wchunk ^ (W8 ? 0 : 4 * (i & 1)));
   }
-  const char* bx = (const char*)a.x + (int64_t)m0 * xrow;
+  const char* bx = (const char*)a.x + (int64_t)m0 * xrow + wk * kXRow;
   const char* bw[2];   // of each half of the wave's weight rows
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int mat = GATED ? ((w * NW + h * (NW / 2)) * WRPL >> 5) & 1 : 0;
-    bw[h] = (const char*)(mat ? a.W[1] : a.W[0]) + (int64_t)n0 * wrow;
+    bw[h] = (const char*)(mat ? a.W[1] : a.W[0]) + (int64_t)n0 * wrow + wk * TT::WROW;
   }
-  const int nk = (a.K + TT::BK - 1) / TT::BK, nfull = a.K / TT::BK;
+  // Step t of the group is step WK t + wk of K; steps are full below nfull in every group, and
+  // every group takes nk steps (past K: zeros).
+  const int nk = (a.K + WK * TT::BK - 1) / (WK * TT::BK), nfull = a.K / (WK * TT::BK);
   // Load i (x part, then weight part) of step t into the part at LDS byte `part`; a last step
   // that K does not fill (tail) has zeros past K.
   auto load = [&](auto tail, int i, int t, int part) {
     const bool isx = i < NX;
     const int q = isx ? i : i - NX;
-    const uint32_t dst = (uint32_t)(part + (w * (isx ? NX : NW) + q) * 1024);
+    const uint32_t dst = (uint32_t)(lds0 + part + (w * (isx ? NX : NW) + q) * 1024);
     const char* base = isx ? bx : bw[q >= NW / 2 && NW > 1 ? 1 : 0];
     const uint32_t off = isx ? ox[isx ? q : 0] : ow[isx ? 0 : q];
     if constexpr (decltype(tail)::value) {
       const int chunk = isx ? xchunk ^ (4 * (q & 1)) : wchunk ^ (W8 ? 0 : 4 * (q & 1));
-      const int k = t * TT::BK + chunk * (16 / (int)(isx ? sizeof(XT) : sizeof(WT)));
+      const int k = (t * WK + wk) * TT::BK + chunk * (16 / (int)(isx ? sizeof(XT) : sizeof(WT)));
       if (k < a.K)
         load_to_lds(base, off, dst);
       else
@@ -341,10 +367,10 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearArgs a)
     } else {
       load_to_lds(base, off, dst);
     }
-    if (i == NX - 1) bx += kXRow;
+    if (i == NX - 1) bx += WK * kXRow;
     if (i == NX + NW - 1) {
-      bw[0] += TT::WROW;
-      bw[1] += TT::WROW;
+      bw[0] += WK * TT::WROW;
+      bw[1] += WK * TT::WROW;
     }
   };
   auto load_part = [&](int from, int to, int t, int part) {
@@ -362,8 +388,8 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearArgs a)
   // Operand reads: row lane % 16 of a 16-row block, chunk lane / 16 of the slice.
   constexpr int XB = 2 * MB, WB = 2 * NB;
   const int fr = lane & 15, fg = lane >> 4;
-  const int xrd = (wm * 32 * MB + fr) * kXRow, xsw = 16 * (fg ^ ((fr >> 1) & 7));
-  const int wrd = (wn * 32 * NB + fr) * TT::WROW;
+  const int xrd = lds0 + (wm * 32 * MB + fr) * kXRow, xsw = 16 * (fg ^ ((fr >> 1) & 7));
+  const int wrd = lds0 + (wn * 32 * NB + fr) * TT::WROW;
   const int wsw = W8 ? 16 * ((fg >> 1) ^ ((fr >> 2) & 3)) : xsw;
   u32x4 xf[2][XB];
   typename TT::WReg wf[2][WB];
@@ -477,7 +503,25 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearArgs a)
   for (; t + ST < nfull; ++t) step(std::true_type{}, t);
   for (; t < nk; ++t) step(std::false_type{}, t);
   wait_loads();
-  stage_barrier();   // the stages are free for the transposes
+  stage_barrier();   // the stages are free for what follows
+  if constexpr (WK > 1) {
+    // the groups' sums, added in order by the first group
+    float* sums = (float*)smem + ((wk - 1) * WM * WN + w) * (64 * 4 * XB * WB) + lane * 4;
+    if (wk > 0) {
+#pragma unroll
+      for (int i = 0; i < XB * WB; ++i)
+        *reinterpret_cast<floatx4*>(sums + i * 256) = acc[i / WB][i % WB];
+    }
+    __syncthreads();
+    if (wk > 0) return;
+#pragma unroll
+    for (int q = 1; q < WK; ++q) {
+      sums = (float*)smem + ((q - 1) * WM * WN + w) * (64 * 4 * XB * WB) + lane * 4;
+#pragma unroll
+      for (int i = 0; i < XB * WB; ++i)
+        acc[i / WB][i % WB] += *reinterpret_cast<const floatx4*>(sums + i * 256);
+    }
+  }
 
   // Epilogue, a wave by itself: the sums of 32 rows at a time through LDS, so that a lane
   // finishes 8 neighbouring columns of a row and rows leave in whole segments.  The lane's
@@ -486,7 +530,7 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearArgs a)
   // name the accumulators), as it holds every activation.
   constexpr int LD = tile_epilogue_ld<NB>(), WC = 32 * NB / (GATED ? 2 : 1), PER = WC / 8;
   constexpr int STEP = 64 / PER;   // rows a wave finishes at a time
-  float* tr = (float*)smem + w * 32 * LD;
+  float* tr = (float*)smem + (WK - 1) * WM * WN * 64 * 4 * XB * WB + w * 32 * LD;
   const int c = lane % PER * 8, n = n0 + wn * WC + c, row0 = lane / PER;
   const float* z = tr + (GATED ? 64 * (c >> 5) + (c & 31) : c);   // gated: up sums 32 further
   Columns cg, cu;
@@ -552,22 +596,22 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearArgs a)
 }
 
 // The LDS of a tile kernel is above the default limit: raised once per device and kernel.
-template <typename WT, int MB, int NB, int WM, int WN, int ST, bool GATED>
+template <typename WT, int MB, int NB, int WM, int WN, int WK, int ST, bool GATED>
 static hipError_t run_tiles(const LinearArgs& a, hipStream_t s) {
   static std::atomic<bool> done[kMaxDevices];
-  constexpr int lds = tile_lds_bytes<WT, MB, NB, WM, WN, ST>();
+  constexpr int lds = tile_lds_bytes<WT, MB, NB, WM, WN, WK, ST>();
   int dev = 0;
   hipError_t e = hipGetDevice(&dev);
   if (e != hipSuccess) return e;
   if (dev < 0 || dev >= kMaxDevices || !done[dev].load(std::memory_order_acquire)) {
-    e = hipFuncSetAttribute((const void*)linear_tile_kernel<WT, MB, NB, WM, WN, ST, GATED>,
+    e = hipFuncSetAttribute((const void*)linear_tile_kernel<WT, MB, NB, WM, WN, WK, ST, GATED>,
                             hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) return e;
     if (dev >= 0 && dev < kMaxDevices) done[dev].store(true, std::memory_order_release);
   }
   const int64_t tiles = ceil_div(a.M, tile_m<MB, WM>()) * ceil_div(a.N, tile_n<NB, WN, GATED>());
-  hipLaunchKernelGGL((linear_tile_kernel<WT, MB, NB, WM, WN, ST, GATED>), dim3((unsigned)tiles),
-                     dim3(64 * WM * WN), lds, s, a);
+  hipLaunchKernelGGL((linear_tile_kernel<WT, MB, NB, WM, WN, WK, ST, GATED>), dim3((unsigned)tiles),
+                     dim3(64 * WM * WN * WK), lds, s, a);
   return hipGetLastError();
 }
 
@@ -596,19 +640,34 @@ static hipError_t launch_rows(const LinearArgs& a, hipStream_t s) {
 template <typename WT, bool GATED>
 static hipError_t launch_linear_t(const LinearArgs& a, hipStream_t s) {
   if (a.M <= 16) return launch_rows<WT, GATED>(a, s);
-  // Largest tile (x rows by weight rows) that still gives every CU one; below that, what gives
-  // the most.  Tiles taller than 64 address their rows from the first with 32 bits.
-  const int64_t cus = device_cu_count(), out = GATED ? 2 : 1;
-  const int64_t row = std::max(a.ldx * (int64_t)sizeof(typename Tile<WT>::X),
-                               a.ldw * (int64_t)sizeof(WT));
-  const bool near_rows = row * 256 < ((int64_t)1 << 32);
-  auto fills = [&](int m, int n) {
-    return near_rows && ceil_div(a.M, m) * ceil_div(a.N * out, n) >= cus;
+  // The tile (x rows by weight rows) with the least estimated time: rounds of tiles over the
+  // CUs times the clocks of a tile, its steps (the slower of the loads at 45 bytes a clock
+  // and CU and of the MFMAs) and a prologue and epilogue that grow with it.  Against the
+  // largest tile that fills the CUs: 64 x 7168 x 2048 takes 64 x 32 tiles, 224 of them (one
+  // round), not 448 of 32 x 32 (11.7 us), and 256 x 14336 x 4096 takes 224 tiles of 128 x 128
+  // instead of 896 of 64 x 64 (49 us).
+  constexpr int out = GATED ? 2 : 1;   // weight rows per output column
+  typedef Tile<WT> TT;
+  const int64_t cus = device_cu_count(), steps = ceil_div(a.K, TT::BK);
+  const int64_t row = std::max(a.ldx * (int64_t)sizeof(typename TT::X), a.ldw * (int64_t)sizeof(WT));
+  const bool near_rows = row * 256 < ((int64_t)1 << 32);   // for tiles taller than 64
+  auto clocks = [&](int m, int w) -> double {
+    if (m > 64 && !near_rows) return 1e300;
+    const double loads = (m * (double)kXRow + w * (double)TT::WROW) / 45.0;
+    const double mma = m * (double)w / (sizeof(WT) == 4 ? 3.4 : 24.0);
+    const double tile = steps * std::max(loads, mma) + 4000.0 + m * (double)w / 4.0;
+    return (double)ceil_div(ceil_div(a.M, m) * ceil_div(a.N * (int64_t)out, w), cus) * tile;
   };
-  if (fills(256, 256)) return run_tiles<WT, 4, 2, 2, 4, 2, GATED>(a, s);
-  if (fills(256, 128)) return run_tiles<WT, 2, 2, 4, 2, 3, GATED>(a, s);
-  if (fills(128, 128)) return run_tiles<WT, 2, 2, 2, 2, 2, GATED>(a, s);
-  return run_tiles<WT, 1, GATED ? 2 : 1, 2, 2, GATED ? 3 : 4, GATED>(a, s);
+  const double t[] = {clocks(256, 256), clocks(256, 128),      clocks(128, 128),
+                      clocks(64, 64 * out), clocks(64, 32 * out), clocks(32, 32 * out)};
+  switch ((int)(std::min_element(t, t + 6) - t)) {
+    case 0: return run_tiles<WT, 4, 2, 2, 4, 1, 2, GATED>(a, s);
+    case 1: return run_tiles<WT, 2, 2, 4, 2, 1, 3, GATED>(a, s);
+    case 2: return run_tiles<WT, 2, 2, 2, 2, 1, 2, GATED>(a, s);
+    case 3: return run_tiles<WT, 1, out, 2, 2, 1, GATED ? 3 : 4, GATED>(a, s);
+    case 4: return run_tiles<WT, 1, out, 2, 1, 2, GATED ? 3 : 4, GATED>(a, s);
+    default: return run_tiles<WT, 1, out, 1, 1, 4, GATED ? 2 : 4, GATED>(a, s);
+  }
 }
 
 template <typename WT>
