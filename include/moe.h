@@ -338,28 +338,21 @@ typedef struct {
 
 /* Host-only check of a description with plain weights (fp8 == 0) or 8-bit ones. */
 moe_status_t moe_linear_validate(const moe_linear_desc_t* desc, int fp8);
-/* Bytes of workspace a call takes (256-byte aligned; gated and fp8 as for the entry point
- * called); 0: none, NULL may be passed (also for an invalid description).  No HIP call
- * but the CU count of the current device. */
-size_t moe_linear_workspace_bytes(const moe_linear_desc_t* desc, int gated, int fp8);
-/* Errors: MOE_E_NULL (x, W, scales, out), MOE_E_SHAPE, MOE_E_UNSUPPORTED, MOE_E_WORKSPACE,
+/* No workspace.  Errors: MOE_E_NULL (x, W, scales, out), MOE_E_SHAPE, MOE_E_UNSUPPORTED,
  * MOE_E_HIP. */
 moe_status_t moe_linear(const moe_linear_desc_t* desc, const void* x, const void* W,
-                        const float* bias, const void* residual, void* out, void* workspace,
-                        size_t workspace_bytes, void* stream);
+                        const float* bias, const void* residual, void* out, void* stream);
 moe_status_t moe_linear_gated(const moe_linear_desc_t* desc, const void* x, const void* W_gate,
                               const void* W_up, const float* bias_gate, const float* bias_up,
-                              const void* residual, void* out, void* workspace,
-                              size_t workspace_bytes, void* stream);
+                              const void* residual, void* out, void* stream);
 moe_status_t moe_linear_fp8(const moe_linear_desc_t* desc, const void* x, const uint8_t* Wq,
                             const float* s, const float* bias, const void* residual, void* out,
-                            void* workspace, size_t workspace_bytes, void* stream);
+                            void* stream);
 moe_status_t moe_linear_gated_fp8(const moe_linear_desc_t* desc, const void* x,
                                   const uint8_t* Wq_gate, const uint8_t* Wq_up,
                                   const float* s_gate, const float* s_up,
                                   const float* bias_gate, const float* bias_up,
-                                  const void* residual, void* out, void* workspace,
-                                  size_t workspace_bytes, void* stream);
+                                  const void* residual, void* out, void* stream);
 
 /* ---- The layer for a few tokens: at most MOE_FEW_TOKENS of them, as in single-token or
  * small-batch decoding, where moe_forward is bound by its launches and by one workgroup's

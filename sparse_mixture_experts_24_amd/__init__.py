@@ -38,8 +38,8 @@ EXPORTS = ("moe_status_str", "moe_validate", "moe_workspace_bytes", "moe_capacit
            "moe_workspace_bytes_expert_choice", "moe_capacity_expert_choice",
            "moe_route_expert_choice", "moe_combine_expert_choice", "moe_forward_expert_choice",
            "moe_forward_next_best", "moe_route_next_best", "moe_dispatch_next_best",
-           "moe_forward_noalloc", "moe_linear_validate", "moe_linear_workspace_bytes",
-           "moe_linear", "moe_linear_gated", "moe_linear_fp8", "moe_linear_gated_fp8",
+           "moe_forward_noalloc", "moe_linear_validate", "moe_linear",
+           "moe_linear_gated", "moe_linear_fp8", "moe_linear_gated_fp8",
            "moe_workspace_bytes_few", "moe_forward_few", "moe_forward_few_fp8")
 # Most tokens of a forward_few call (moe.h).
 FEW_TOKENS = 16
@@ -137,16 +137,14 @@ def lib():
         LD = ctypes.POINTER(LinearDesc)
         L.moe_linear_validate.restype = I
         L.moe_linear_validate.argtypes = [LD, I]
-        L.moe_linear_workspace_bytes.restype = S
-        L.moe_linear_workspace_bytes.argtypes = [LD, I, I]
         L.moe_linear.restype = I
-        L.moe_linear.argtypes = [LD, P, P, P, P, P, P, S, P]
+        L.moe_linear.argtypes = [LD, P, P, P, P, P, P]
         L.moe_linear_gated.restype = I
-        L.moe_linear_gated.argtypes = [LD, P, P, P, P, P, P, P, P, S, P]
+        L.moe_linear_gated.argtypes = [LD, P, P, P, P, P, P, P, P]
         L.moe_linear_fp8.restype = I
-        L.moe_linear_fp8.argtypes = [LD, P, P, P, P, P, P, P, S, P]
+        L.moe_linear_fp8.argtypes = [LD, P, P, P, P, P, P, P]
         L.moe_linear_gated_fp8.restype = I
-        L.moe_linear_gated_fp8.argtypes = [LD, P, P, P, P, P, P, P, P, P, P, S, P]
+        L.moe_linear_gated_fp8.argtypes = [LD, P, P, P, P, P, P, P, P, P, P]
         L.moe_workspace_bytes_few.restype = S
         L.moe_workspace_bytes_few.argtypes = [D]
         L.moe_forward_few.restype = I
@@ -670,44 +668,59 @@ def alloc_workspace_few(desc: MoeDesc, device) -> torch.Tensor:
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
+def _raw_stream(dev):
+    """The current HIP stream of dev as an integer, without a Stream object around it (2 us)."""
+    return torch._C._cuda_getCurrentRawStream(dev.index)
+
+
+def _need(t, name, dev, dtype, shape):
+    """_require in one pass over the usual case: small calls are bound by the host."""
+    if t.device != dev or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        _require(t, name, dev, dtype, shape)
+
+
 def _few(name, x, W_router, bias, weights, scales, k, capacity_factor, residual, out, f, p,
          out_dtype, workspace, want_stats):
-    dev = x.device
-    T, d = x.shape
-    E = W_router.shape[0]
-    G, F, _ = weights[0].shape
-    odt = out_dtype or x.dtype
-    wdt = x.dtype if scales is None else torch.uint8
-    desc = make_desc(T, d, E, F, k, G - E, capacity_factor, x.dtype, odt)
-    _require(x, "x", dev)
-    _require(W_router, "W_router", dev, x.dtype, (E, d))
-    _require(bias, "router_bias", dev, torch.float32, (E,))
-    for w, n, shape in zip(weights, ("W_gate", "W_up", "W_down"),
-                           ((G, F, d), (G, F, d), (G, d, F))):
-        _require(w, n, dev, wdt, shape)
-    for s, n, shape in zip(scales or (), ("s_gate", "s_up", "s_down"), ((G, F), (G, F), (G, d))):
-        _require(s, n, dev, torch.float32, shape)
-    _require(residual, "residual", dev, odt, (T, d))
-    _require(out, "out", dev, odt, (T, d))
-    _require(f, "f", dev, torch.float32, (E,))
-    _require(p, "p", dev, torch.float32, (E,))
+    dev, dt = x.device, x.dtype
     if dev.index != torch.cuda.current_device():
         with torch.cuda.device(dev):
             return _few(name, x, W_router, bias, weights, scales, k, capacity_factor, residual,
                         out, f, p, out_dtype, workspace, want_stats)
+    T, d = x.shape
+    E = W_router.shape[0]
+    G, F, _ = weights[0].shape
+    odt = out_dtype or dt
+    desc = MoeDesc(T, d, E, F, k, G - E, capacity_factor, _dt(dt), _dt(odt))
+    _need(x, "x", dev, dt, (T, d))
+    _need(W_router, "W_router", dev, dt, (E, d))
+    wdt, up, down = dt if scales is None else torch.uint8, (G, F, d), (G, d, F)
+    _need(weights[0], "W_gate", dev, wdt, up)
+    _need(weights[1], "W_up", dev, wdt, up)
+    _need(weights[2], "W_down", dev, wdt, down)
+    args = [x.data_ptr(), W_router.data_ptr(), None, *[w.data_ptr() for w in weights]]
+    if bias is not None:
+        _need(bias, "router_bias", dev, torch.float32, (E,))
+        args[2] = bias.data_ptr()
+    if scales is not None:
+        for s, n, shape in zip(scales, ("s_gate", "s_up", "s_down"), (up[:2], up[:2], down[:2])):
+            _need(s, n, dev, torch.float32, shape)
+            args.append(s.data_ptr())
+    for t, n, tdt, shape in ((residual, "residual", odt, (T, d)), (out, "out", odt, (T, d)),
+                             (f, "f", torch.float32, (E,)), (p, "p", torch.float32, (E,))):
+        if t is not None:
+            _need(t, n, dev, tdt, shape)
     if out is None:
         out = torch.empty(T, d, dtype=odt, device=dev)
-    if want_stats and f is None:
-        f = torch.empty(E, dtype=torch.float32, device=dev)
-    if want_stats and p is None:
-        p = torch.empty(E, dtype=torch.float32, device=dev)
+    if want_stats:
+        if f is None:
+            f = torch.empty(E, dtype=torch.float32, device=dev)
+        if p is None:
+            p = torch.empty(E, dtype=torch.float32, device=dev)
     if workspace is None:
         workspace = alloc_workspace_few(desc, dev)
-    args = [x.data_ptr(), W_router.data_ptr(), _opt_ptr(bias), *[w.data_ptr() for w in weights],
-            *[s.data_ptr() for s in scales or ()], _opt_ptr(residual), out.data_ptr(),
-            _opt_ptr(f), _opt_ptr(p), workspace.data_ptr(), workspace.numel(),
-            torch.cuda.current_stream(dev).cuda_stream]
-    _check(name, getattr(lib(), name)(ctypes.byref(desc), *args))
+    args += [_opt_ptr(residual), out.data_ptr(), _opt_ptr(f), _opt_ptr(p), workspace.data_ptr(),
+             workspace.numel(), _raw_stream(dev)]
+    _check(name, getattr(lib(), name)(desc, *args))
     return out, f, p
 
 
@@ -730,17 +743,19 @@ def forward_few_fp8(x, W_router, router_bias, Wq_gate, Wq_up, Wq_down, s_gate, s
 
 
 # ----------------------------------------------------------------------------- dense products
-def _rows(t, name, device, dtype, shape):
+def _rows(t, name, dev, dtype, shape):
     """Checks a [rows, cols] tensor whose rows may be strided; returns its row stride."""
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if t.dtype != dtype:
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if t.dtype is not dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if shape[1] > 1 and t.stride(1) != 1:
+    ld, inner = t.stride()
+    if shape[1] > 1 and inner != 1:
         raise ValueError(f"{name} must have contiguous rows")
-    ld = t.stride(0) if shape[0] > 1 else shape[1]
+    if shape[0] < 2:
+        return shape[1]
     if ld < shape[1]:
         raise ValueError(f"{name} has overlapping rows (row stride {ld})")
     return ld
@@ -752,84 +767,68 @@ def _opt_ptr(t):
 
 def linear_desc(x, W, act="none", residual=None, out=None, out_dtype=None, fp8=False):
     """Description of a dense product of x [M, K] and W [N, K] (strides as the tensors')."""
-    dev = x.device
     if x.dim() != 2 or W.dim() != 2:
         raise ValueError("x and W must be matrices")
     if act not in ACTS:
         raise ValueError(f"act {act!r} is none of {', '.join(ACTS)}")
+    dev, dt, odt = x.device, x.dtype, out_dtype or x.dtype
     M, K = x.shape
     N = W.shape[0]
-    odt = out_dtype or x.dtype
-    ldx = _rows(x, "x", dev, x.dtype, (M, K))
-    ldw = _rows(W, "W", dev, torch.uint8 if fp8 else x.dtype, (N, K))
-    ldr = 0 if residual is None else _rows(residual, "residual", dev, odt, (M, N))
-    ldo = 0 if out is None else _rows(out, "out", dev, odt, (M, N))
-    return LinearDesc(M, N, K, ldx, ldw, ldr, ldo, _dt(x.dtype), _dt(odt), ACTS[act])
+    return LinearDesc(M, N, K, _rows(x, "x", dev, dt, (M, K)),
+                      _rows(W, "W", dev, torch.uint8 if fp8 else dt, (N, K)),
+                      0 if residual is None else _rows(residual, "residual", dev, odt, (M, N)),
+                      0 if out is None else _rows(out, "out", dev, odt, (M, N)),
+                      _dt(dt), _dt(odt), ACTS[act])
 
 
-def linear_workspace_bytes(desc: LinearDesc, gated=False, fp8=False) -> int:
-    """Bytes of workspace such a call takes (0: none)."""
-    return int(lib().moe_linear_workspace_bytes(ctypes.byref(desc), int(gated), int(fp8)))
-
-
-def _linear(name, x, W, W2, s, s2, b, b2, act, residual, out, out_dtype, workspace):
-    gated, fp8 = W2 is not None, s is not None
-    desc = linear_desc(x, W, act, residual, out, out_dtype, fp8)
-    dev, N = x.device, desc.N
-    if gated and _rows(W2, "W_up", dev, W.dtype, W.shape) != desc.ldw:
-        raise ValueError("W_gate and W_up must have the same row stride")
-    for t, n in ((b, "bias"), (b2, "bias_up"), (s, "s"), (s2, "s_up")):
-        if t is not None:
-            _require(t, n, dev, torch.float32, (N,))
+def _linear(name, x, W, W2, s, s2, b, b2, act, residual, out, out_dtype):
+    dev = x.device
     if dev.index != torch.cuda.current_device():
         with torch.cuda.device(dev):
-            return _linear(name, x, W, W2, s, s2, b, b2, act, residual, out, out_dtype, workspace)
-    if out is None:
-        out = torch.empty(x.shape[0], N, dtype=out_dtype or x.dtype, device=dev)
-    if workspace is None:
-        n = linear_workspace_bytes(desc, gated, fp8)
-        workspace = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+            return _linear(name, x, W, W2, s, s2, b, b2, act, residual, out, out_dtype)
+    desc = linear_desc(x, W, act, residual, out, out_dtype, s is not None)
+    N = desc.N
     args = [x.data_ptr(), W.data_ptr()]
-    if gated:
+    if W2 is not None:
+        if _rows(W2, "W_up", dev, W.dtype, W.shape) != desc.ldw:
+            raise ValueError("W_gate and W_up must have the same row stride")
         args.append(W2.data_ptr())
-    if fp8:
-        args.append(s.data_ptr())
-        if gated:
-            args.append(s2.data_ptr())
-    args.append(_opt_ptr(b))
-    if gated:
-        args.append(_opt_ptr(b2))
-    args += [_opt_ptr(residual), out.data_ptr(), _opt_ptr(workspace),
-             0 if workspace is None else workspace.numel(),
-             torch.cuda.current_stream(dev).cuda_stream]
-    _check(name, getattr(lib(), name)(ctypes.byref(desc), *args))
+    for t, n, have in ((s, "s", True), (s2, "s_up", True), (b, "bias", False),
+                       (b2, "bias_up", False)):
+        if t is not None:
+            _need(t, n, dev, torch.float32, (N,))
+            args.append(t.data_ptr())
+        elif not have and (W2 is not None or n == "bias"):
+            args.append(None)
+    if out is None:
+        out = torch.empty(desc.M, N, dtype=out_dtype or x.dtype, device=dev)
+    _check(name, getattr(lib(), name)(desc, *args, _opt_ptr(residual), out.data_ptr(),
+                                      _raw_stream(dev)))
     return out
 
 
-def linear(x, W, bias=None, act="none", residual=None, out=None, out_dtype=None, workspace=None):
+def linear(x, W, bias=None, act="none", residual=None, out=None, out_dtype=None):
     """act(x W^T + bias) + residual: x [M, K], W [N, K] (rows of either, of residual and of
     out may be strided), bias [N] float32, residual and out [M, N] in out_dtype.  residual may
     be out itself.  Returns out."""
-    return _linear("moe_linear", x, W, None, None, None, bias, None, act, residual, out,
-                   out_dtype, workspace)
+    return _linear("moe_linear", x, W, None, None, None, bias, None, act, residual, out, out_dtype)
 
 
 def linear_gated(x, W_gate, W_up, bias_gate=None, bias_up=None, act="silu", residual=None,
-                 out=None, out_dtype=None, workspace=None):
+                 out=None, out_dtype=None):
     """act(x W_gate^T + bias_gate) * (x W_up^T + bias_up) + residual; arguments as linear."""
     return _linear("moe_linear_gated", x, W_gate, W_up, None, None, bias_gate, bias_up, act,
-                   residual, out, out_dtype, workspace)
+                   residual, out, out_dtype)
 
 
-def linear_fp8(x, Wq, s, bias=None, act="none", residual=None, out=None, out_dtype=None,
-               workspace=None):
+def linear_fp8(x, Wq, s, bias=None, act="none", residual=None, out=None, out_dtype=None):
     """linear with W = s * decode(Wq): e4m3 codes [N, K] uint8, one float32 scale per row."""
     return _linear("moe_linear_fp8", x, Wq, None, s, None, bias, None, act, residual, out,
-                   out_dtype, workspace)
+                   out_dtype)
 
 
 def linear_gated_fp8(x, Wq_gate, Wq_up, s_gate, s_up, bias_gate=None, bias_up=None, act="silu",
-                     residual=None, out=None, out_dtype=None, workspace=None):
+                     residual=None, out=None, out_dtype=None):
     """linear_gated with 8-bit weights, as linear_fp8."""
     return _linear("moe_linear_gated_fp8", x, Wq_gate, Wq_up, s_gate, s_up, bias_gate, bias_up,
-                   act, residual, out, out_dtype, workspace)
+                   act, residual, out, out_dtype)

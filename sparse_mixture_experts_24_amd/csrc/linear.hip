@@ -644,26 +644,29 @@ static hipError_t launch_linear_t(const LinearArgs& a, hipStream_t s) {
   // CUs times the clocks of a tile, its steps (the slower of the loads at 45 bytes a clock
   // and CU and of the MFMAs) and a prologue and epilogue that grow with it.  Against the
   // largest tile that fills the CUs: 64 x 7168 x 2048 takes 64 x 32 tiles, 224 of them (one
-  // round), not 448 of 32 x 32 (11.7 us), and 256 x 14336 x 4096 takes 224 tiles of 128 x 128
-  // instead of 896 of 64 x 64 (49 us).
+  // round, 8.1 us), not 448 of 32 x 32 (11.7 us); 256 x 14336 x 4096 takes 224 tiles of 128 x
+  // 128 (35.7 us) instead of 896 of 64 x 64 (49 us), but 512 x 4096 x 4096 takes 512 tiles of
+  // 64 x 64 (27 us), not 128 of 128 x 128 (32 us).
   constexpr int out = GATED ? 2 : 1;   // weight rows per output column
   typedef Tile<WT> TT;
   const int64_t cus = device_cu_count(), steps = ceil_div(a.K, TT::BK);
   const int64_t row = std::max(a.ldx * (int64_t)sizeof(typename TT::X), a.ldw * (int64_t)sizeof(WT));
   const bool near_rows = row * 256 < ((int64_t)1 << 32);   // for tiles taller than 64
-  auto clocks = [&](int m, int w) -> double {
+  // per: products that a CU does in a clock on such a tile, as measured in bf16
+  auto clocks = [&](int m, int w, double per) -> double {
     if (m > 64 && !near_rows) return 1e300;
     const double loads = (m * (double)kXRow + w * (double)TT::WROW) / 45.0;
-    const double mma = m * (double)w / (sizeof(WT) == 4 ? 3.4 : 24.0);
+    const double mma = m * (double)w / (sizeof(WT) == 4 ? 3.4 : per / 64);
     const double tile = steps * std::max(loads, mma) + 4000.0 + m * (double)w / 4.0;
     return (double)ceil_div(ceil_div(a.M, m) * ceil_div(a.N * (int64_t)out, w), cus) * tile;
   };
-  const double t[] = {clocks(256, 256), clocks(256, 128),      clocks(128, 128),
-                      clocks(64, 64 * out), clocks(64, 32 * out), clocks(32, 32 * out)};
+  const double t[] = {clocks(256, 256, 1536),     clocks(256, 128, 1280),
+                      clocks(128, 128, 1024),     clocks(64, 64 * out, 1024),
+                      clocks(64, 32 * out, 1024), clocks(32, 32 * out, 1024)};
   switch ((int)(std::min_element(t, t + 6) - t)) {
     case 0: return run_tiles<WT, 4, 2, 2, 4, 1, 2, GATED>(a, s);
     case 1: return run_tiles<WT, 2, 2, 4, 2, 1, 3, GATED>(a, s);
-    case 2: return run_tiles<WT, 2, 2, 2, 2, 1, 2, GATED>(a, s);
+    case 2: return run_tiles<WT, 1, 2, 4, 2, 1, 4, GATED>(a, s);
     case 3: return run_tiles<WT, 1, out, 2, 2, 1, GATED ? 3 : 4, GATED>(a, s);
     case 4: return run_tiles<WT, 1, out, 2, 1, 2, GATED ? 3 : 4, GATED>(a, s);
     default: return run_tiles<WT, 1, out, 1, 1, 4, GATED ? 2 : 4, GATED>(a, s);
@@ -712,8 +715,7 @@ static bool aligned_to(const void* p, uintptr_t n) { return ((uintptr_t)p & (n -
 static moe_status_t linear_impl(const moe_linear_desc_t* desc, const void* x, const void* W0,
                                 const void* W1, const float* s0, const float* s1,
                                 const float* b0, const float* b1, const void* residual,
-                                void* out, void* workspace, size_t workspace_bytes, void* stream,
-                                bool gated, bool fp8) {
+                                void* out, void* stream, bool gated, bool fp8) {
   moe_status_t st = validate_linear(desc, fp8);
   if (st != MOE_OK) return st;
   const moe_linear_desc_t& d = *desc;
@@ -724,8 +726,6 @@ static moe_status_t linear_impl(const moe_linear_desc_t* desc, const void* x, co
       !aligned_to(s1, 4) || !aligned_to(b0, 4) || !aligned_to(b1, 4) ||
       !aligned_to(residual, ob) || !aligned_to(out, ob))
     return MOE_E_UNSUPPORTED;
-  (void)workspace;
-  (void)workspace_bytes;
   if (d.M == 0) return MOE_OK;
   const LinearArgs a{x,
                      {W0, W1},
@@ -758,43 +758,33 @@ moe_status_t moe_linear_validate(const moe_linear_desc_t* desc, int fp8) {
   return validate_linear(desc, fp8 != 0);
 }
 
-size_t moe_linear_workspace_bytes(const moe_linear_desc_t* desc, int gated, int fp8) {
-  (void)desc;
-  (void)gated;
-  (void)fp8;
-  return 0;
-}
-
 moe_status_t moe_linear(const moe_linear_desc_t* desc, const void* x, const void* W,
-                        const float* bias, const void* residual, void* out, void* workspace,
-                        size_t workspace_bytes, void* stream) {
-  return linear_impl(desc, x, W, nullptr, nullptr, nullptr, bias, nullptr, residual, out,
-                     workspace, workspace_bytes, stream, false, false);
+                        const float* bias, const void* residual, void* out, void* stream) {
+  return linear_impl(desc, x, W, nullptr, nullptr, nullptr, bias, nullptr, residual, out, stream,
+                     false, false);
 }
 
 moe_status_t moe_linear_gated(const moe_linear_desc_t* desc, const void* x, const void* W_gate,
                               const void* W_up, const float* bias_gate, const float* bias_up,
-                              const void* residual, void* out, void* workspace,
-                              size_t workspace_bytes, void* stream) {
+                              const void* residual, void* out, void* stream) {
   return linear_impl(desc, x, W_gate, W_up, nullptr, nullptr, bias_gate, bias_up, residual, out,
-                     workspace, workspace_bytes, stream, true, false);
+                     stream, true, false);
 }
 
 moe_status_t moe_linear_fp8(const moe_linear_desc_t* desc, const void* x, const uint8_t* Wq,
                             const float* s, const float* bias, const void* residual, void* out,
-                            void* workspace, size_t workspace_bytes, void* stream) {
-  return linear_impl(desc, x, Wq, nullptr, s, nullptr, bias, nullptr, residual, out, workspace,
-                     workspace_bytes, stream, false, true);
+                            void* stream) {
+  return linear_impl(desc, x, Wq, nullptr, s, nullptr, bias, nullptr, residual, out, stream, false,
+                     true);
 }
 
 moe_status_t moe_linear_gated_fp8(const moe_linear_desc_t* desc, const void* x,
                                   const uint8_t* Wq_gate, const uint8_t* Wq_up,
                                   const float* s_gate, const float* s_up,
                                   const float* bias_gate, const float* bias_up,
-                                  const void* residual, void* out, void* workspace,
-                                  size_t workspace_bytes, void* stream) {
+                                  const void* residual, void* out, void* stream) {
   return linear_impl(desc, x, Wq_gate, Wq_up, s_gate, s_up, bias_gate, bias_up, residual, out,
-                     workspace, workspace_bytes, stream, true, true);
+                     stream, true, true);
 }
 
 }  // extern "C"

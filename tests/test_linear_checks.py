@@ -63,24 +63,24 @@ def test_descriptions(L, kw, plain, fp8):
 def test_null_and_misaligned_arguments(L):
     f, odd, P = 0x100000, 0x100004, ctypes.byref(desc())
     assert L.moe_linear_validate(None, 0) == 1
-    assert L.moe_linear(None, f, f, None, None, f, None, 0, None) == 1
-    assert L.moe_linear(P, None, f, None, None, f, None, 0, None) == 1
-    assert L.moe_linear(P, f, None, None, None, f, None, 0, None) == 1
-    assert L.moe_linear(P, f, f, None, None, None, None, 0, None) == 1
-    assert L.moe_linear_gated(P, f, f, None, None, None, None, f, None, 0, None) == 1
-    assert L.moe_linear_fp8(P, f, f, None, None, None, f, None, 0, None) == 1
-    assert L.moe_linear_gated_fp8(P, f, f, f, f, None, None, None, None, f, None, 0, None) == 1
-    assert L.moe_linear(P, odd, f, None, None, f, None, 0, None) == 3
-    assert L.moe_linear(P, f, odd, None, None, f, None, 0, None) == 3
-    assert L.moe_linear(P, f, f, odd + 1, None, f, None, 0, None) == 3
-    assert L.moe_linear(P, f, f, None, odd + 1, f, None, 0, None) == 3
-    assert L.moe_linear(P, f, f, None, None, odd + 1, None, 0, None) == 3
-    assert L.moe_linear_gated(P, f, f, odd, None, None, None, f, None, 0, None) == 3
-    assert L.moe_linear_fp8(P, f, f, odd + 2, None, None, f, None, 0, None) == 3
+    assert L.moe_linear(None, f, f, None, None, f, None) == 1
+    assert L.moe_linear(P, None, f, None, None, f, None) == 1
+    assert L.moe_linear(P, f, None, None, None, f, None) == 1
+    assert L.moe_linear(P, f, f, None, None, None, None) == 1
+    assert L.moe_linear_gated(P, f, f, None, None, None, None, f, None) == 1
+    assert L.moe_linear_fp8(P, f, f, None, None, None, f, None) == 1
+    assert L.moe_linear_gated_fp8(P, f, f, f, f, None, None, None, None, f, None) == 1
+    assert L.moe_linear(P, odd, f, None, None, f, None) == 3
+    assert L.moe_linear(P, f, odd, None, None, f, None) == 3
+    assert L.moe_linear(P, f, f, odd + 1, None, f, None) == 3
+    assert L.moe_linear(P, f, f, None, odd + 1, f, None) == 3
+    assert L.moe_linear(P, f, f, None, None, odd + 1, None) == 3
+    assert L.moe_linear_gated(P, f, f, odd, None, None, None, f, None) == 3
+    assert L.moe_linear_fp8(P, f, f, odd + 2, None, None, f, None) == 3
     # no rows: nothing is enqueued, so no tensor but the weights is needed
     zero = ctypes.byref(desc(M=0))
-    assert L.moe_linear(zero, None, f, None, None, None, None, 0, None) == 0
-    assert L.moe_linear(zero, None, None, None, None, None, None, 0, None) == 1
+    assert L.moe_linear(zero, None, f, None, None, None, None) == 0
+    assert L.moe_linear(zero, None, None, None, None, None, None) == 1
 
 
 def test_binding_refuses_what_it_cannot_pass_on():
