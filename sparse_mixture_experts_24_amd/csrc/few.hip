@@ -270,7 +270,7 @@ __global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(FewArgs a) {
     __syncthreads();
     few_route(a, r, lds.route, lds.sums);
   }
-  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63;
   if (blockIdx.x == 0)
     for (int i = tid; i < (int)(sizeof(FewRoute) / 4); i += kFewThreads)
       ((int*)a.route)[i] = ((const int*)&r)[i];
@@ -279,7 +279,7 @@ __global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(FewArgs a) {
   share_of((int64_t)r.nu * upe, blockIdx.x, gridDim.x, i0, i1);
   const int nst = (a.d + S::SK - 1) / S::SK, row_bytes = a.d * (int)sizeof(WT);
   const int nchunk = (nst + NS * kFewWaves - 1) / (NS * kFewWaves);
-  stream_units<WT, NS, R, 1>(
+  stream_units<WT, NS, R, 1, true>(
       i0, i1, nchunk, nst, row_bytes, lds.stream,
       [&](int i, UnitRows& rows) {
         const int u = i / upe;
@@ -289,19 +289,12 @@ __global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(FewArgs a) {
         rows.off[0] = rows.off[1] = (uint32_t)(lane >> 3) * row_bytes;
         return 0;
       },
-      [&](int i, int c, u32x4 (&xs)[1][NS][S::XR]) {
-        if (nchunk == 1 && i > i0) return;   // the same for every unit
-        const int t = lane & 15;
+      [&](TokenRows& x) {
+        x.base = (const char*)a.x;
+        x.k = a.d;
 #pragma unroll
-        for (int s = 0; s < NS; ++s)
-#pragma unroll
-          for (int q = 0; q < S::XR; ++q) {
-            const int k = ((c * NS + s) * kFewWaves + wv) * S::SK + S::k_of(lane >> 4, q);
-            xs[0][s][q] = u32x4{0, 0, 0, 0};
-            if (t < a.T && k < a.d)
-              xs[0][s][q] = *reinterpret_cast<const u32x4*>((const XT*)a.x + (int64_t)t * a.d + k);
-          }
-        landed();
+        for (int h = 0; h < 2; ++h)
+          x.off[h] = (uint32_t)min(8 * h + (lane >> 3), a.T - 1) * (uint32_t)(a.d * sizeof(XT));
       },
       [&](int i, int m, int n, float v) {
         const int u = i / upe, f = i % upe * 8;
@@ -344,7 +337,7 @@ __global__ __launch_bounds__(kFewThreads) void few_down_kernel(FewArgs a) {
   int i0, i1, have = -1;
   share_of((int64_t)r.nu * a.chunks * upc, blockIdx.x, gridDim.x, i0, i1);
   const int nst = (a.F + S::SK - 1) / S::SK, row_bytes = a.F * (int)sizeof(WT);
-  stream_units<WT, NS, R, NH>(
+  stream_units<WT, NS, R, NH, false>(
       i0, i1, 1, nst, row_bytes, lds,
       [&](int i, UnitRows& rows) {
         const int uc = i / upc;
@@ -354,7 +347,7 @@ __global__ __launch_bounds__(kFewThreads) void few_down_kernel(FewArgs a) {
         rows.off[0] = rows.off[1] = (uint32_t)(lane >> 3) * row_bytes;
         return uc % a.chunks * NS * kFewWaves;
       },
-      [&](int i, int, u32x4 (&xs)[NH][NS][S::XR]) {
+      [&](int i, u32x4 (&xs)[NH][NS][S::XR]) {
         const int uc = i / upc;
         if (uc == have) return;
         have = uc;
@@ -498,16 +491,9 @@ static hipError_t launch_few(const FewArgs& a, hipStream_t s) {
   if (a.logits)
     hipLaunchKernelGGL(few_logits_kernel<XT>, dim3((unsigned)ceil_div(a.E, 16), a.ks),
                        dim3(kFewThreads), 0, s, a);
-  if (per <= 2)
-    launch_gate_up_few<WT, 2, 8>(a, s);
-  else if (per <= 4)
-    launch_gate_up_few<WT, 4, 8>(a, s);
-  else if (per <= 8)
-    launch_gate_up_few<WT, 8, 8>(a, s);
-  else if constexpr (sizeof(WT) != 1)
-    launch_gate_up_few<WT, 14, 7>(a, s);
-  else
-    launch_gate_up_few<WT, 8, 8>(a, s);
+  launch_by_steps<WT>(per, [&](auto steps, auto ring) {
+    launch_gate_up_few<WT, decltype(steps)::value, decltype(ring)::value>(a, s);
+  });
   hipLaunchKernelGGL((few_down_kernel<WT, sizeof(WT) == 1 ? kDownSteps / 2 : kDownSteps, 8>),
                      dim3(device_cu_count()), dim3(kFewThreads), 0, s, a);
   hipLaunchKernelGGL(few_join_kernel, dim3((unsigned)ceil_div((int64_t)a.T * a.d, kJoinThreads)),

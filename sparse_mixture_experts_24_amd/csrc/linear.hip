@@ -135,13 +135,13 @@ __global__ __launch_bounds__(kStreamThreads) void linear_rows_kernel(LinearArgs 
   typedef typename S::X XT;
   __shared__ StreamLds<R> lds;
   constexpr int COLS = GATED ? 8 : 16;   // output columns of a unit
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63;
   int i0, i1;
   share_of((a.N + COLS - 1) / COLS, blockIdx.x, gridDim.x, i0, i1);
   const int nst = (a.K + S::SK - 1) / S::SK;
   const int nchunk = (nst + NS * kStreamWaves - 1) / (NS * kStreamWaves);
   const uint32_t wrow = (uint32_t)(a.ldw * (int)sizeof(WT));
-  stream_units<WT, NS, R, 1>(
+  stream_units<WT, NS, R, 1, true>(
       i0, i1, nchunk, nst, a.K * (int)sizeof(WT), lds,
       [&](int i, UnitRows& rows) {
 #pragma unroll
@@ -152,19 +152,12 @@ __global__ __launch_bounds__(kStreamThreads) void linear_rows_kernel(LinearArgs 
         }
         return 0;
       },
-      [&](int i, int c, u32x4 (&xs)[1][NS][S::XR]) {
-        if (nchunk == 1 && i > i0) return;   // the same for every unit
-        const int t = lane & 15;
+      [&](TokenRows& x) {
+        x.base = (const char*)a.x;
+        x.k = a.K;
 #pragma unroll
-        for (int s = 0; s < NS; ++s)
-#pragma unroll
-          for (int q = 0; q < S::XR; ++q) {
-            const int k = ((c * NS + s) * kStreamWaves + wv) * S::SK + S::k_of(lane >> 4, q);
-            xs[0][s][q] = u32x4{0, 0, 0, 0};
-            if (t < a.M && k < a.K)
-              xs[0][s][q] = *reinterpret_cast<const u32x4*>((const XT*)a.x + t * a.ldx + k);
-          }
-        landed();
+        for (int h = 0; h < 2; ++h)
+          x.off[h] = (uint32_t)min(8 * h + (lane >> 3), a.M - 1) * (uint32_t)(a.ldx * (int)sizeof(XT));
       },
       [&](int i, int m, int q, float v) {
         const int n0 = i * COLS, n = n0 + (GATED ? q & 7 : q);
@@ -624,17 +617,13 @@ static hipError_t run_rows(const LinearArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// At most 16 rows: the least number of steps per wave that holds K, so that the token operand
-// stays in registers (K beyond the last runs in chunks).
 template <typename WT, bool GATED>
 static hipError_t launch_rows(const LinearArgs& a, hipStream_t s) {
-  const int64_t per = ceil_div(ceil_div(a.K, Stream<WT>::SK), kStreamWaves);
-  if (per <= 2) return run_rows<WT, 2, 8, GATED>(a, s);
-  if (per <= 4) return run_rows<WT, 4, 8, GATED>(a, s);
-  if constexpr (sizeof(WT) != 1) {   // an 8-bit step takes twice the token operand
-    if (per > 8) return run_rows<WT, 14, 7, GATED>(a, s);
-  }
-  return run_rows<WT, 8, 8, GATED>(a, s);
+  hipError_t e = hipSuccess;
+  launch_by_steps<WT>(ceil_div(ceil_div(a.K, Stream<WT>::SK), kStreamWaves), [&](auto steps, auto ring) {
+    e = run_rows<WT, decltype(steps)::value, decltype(ring)::value, GATED>(a, s);
+  });
+  return e;
 }
 
 template <typename WT, bool GATED>

@@ -177,7 +177,7 @@ struct StreamLds {
 // larger than the 256 MB cache run at 6.5 TB/s so, at 5.7 without.
 template <bool ONCE = false>
 __device__ __forceinline__ void load_to_lds(const char* base, uint32_t off, uint32_t lds) {
-  // nothing else here uses m0
+  lds = __builtin_amdgcn_readfirstlane(lds);   // nothing else here uses m0
   if constexpr (ONCE)
     asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1 nt"
                  :: "v"(off), "s"(base), "s"(lds));
@@ -230,6 +230,14 @@ struct UnitRows {
   uint32_t off[2];       // per lane
 };
 
+// Where the token rows are that do not change from unit to unit: row h * 8 + lane / 8 at
+// base + off[h], k elements (rows past the last token: any row, their sums are not used).
+struct TokenRows {
+  const char* base;   // uniform
+  uint32_t off[2];    // per lane
+  int k;
+};
+
 // Units i0 .. i1 - 1 of 16 weight rows each, against a token operand that stays in registers
 // while it can.  A unit is visited once per chunk of NS steps per wave (NS x 8 steps of the
 // row; one chunk where the row is no longer).  The steps come through a ring of R in LDS,
@@ -237,14 +245,20 @@ struct UnitRows {
 // later one (R divides NS or NS divides R), so a wave always has R x 2 KB in flight and no
 // registers wait for them.
 //   point(i, rows)       where unit i is; returns the row's first step
-//   load_x(i, c, xs)     the wave's token operand of chunk c, xs[0 .. NH - 1] multiplied by
-//                        the same weights (may leave it as it is); ends with landed()
+//   load_x               FIXED tokens: load_x(rows) says where they are.  They come through
+//                        the ring too, before the weights (loaded in operand order, a lane
+//                        per row, 16 rows of 14336 elements take 13 us); with more than one
+//                        chunk every visit starts over, tokens first.
+//                        Else: load_x(i, xs) loads the wave's operand for unit i (or leaves
+//                        it as it is), xs[0 .. NH - 1] multiplied by the same weights, zero
+//                        past the rows' end, and ends with landed(); one chunk only
 //   done(i, m, n, v)     sum v of token m and weight row n of the unit, called by 256 threads
 //                        (whole waves); a vector load there empties the ring
 //   nst, row_bytes       steps and bytes of a weight row
 // Steps past nst repeat its last one and bytes past the row its last chunk (cache hits); the
-// token operand must be zero there.
-template <typename WT, int NS, int R, int NH, typename Point, typename LoadX, typename Done>
+// token operand is zero there.
+template <typename WT, int NS, int R, int NH, bool FIXED, typename Point, typename LoadX,
+          typename Done>
 __device__ __forceinline__ void stream_units(int i0, int i1, int nchunk, int nst, int row_bytes,
                                              StreamLds<R>& lds, Point point, LoadX load_x,
                                              Done done) {
@@ -303,26 +317,85 @@ __device__ __forceinline__ void stream_units(int i0, int i1, int nchunk, int nst
       }
 #pragma unroll
       for (int h = 0; h < NH; ++h) S::mma(acc, xs[h][s], w0, w1);
-      slot = __builtin_amdgcn_readfirstlane(slot == (R - 1) * kStageBytes ? 0 : slot + kStageBytes);
+      slot = slot == (R - 1) * kStageBytes ? 0 : slot + kStageBytes;
     }
   };
   static_assert(R <= 8, "waits");
+  // The first steps of visits v ..: as many as the ring holds, n visits at most.
+  auto fill = [&](int v, int n) {
+    slot = 0;
 #pragma unroll
-  for (int q = 0; q < AHEAD; ++q)
-    if (q < visits) {
-      point_at(q);
+    for (int q = 0; q < AHEAD; ++q)
+      if (q < n) {
+        point_at(v + q);
 #pragma unroll
-      for (int s = 0; s < (R < NS ? R : NS); ++s) load(s, (q * NS + s) * kStageBytes);
+        for (int s = 0; s < (R < NS ? R : NS); ++s) load(s, (q * NS + s) * kStageBytes);
+      }
+  };
+  // Chunk c of the fixed tokens, R ring slots (128 bytes of each row) at a time.
+  TokenRows tokens;
+  if constexpr (FIXED) load_x(tokens);
+  auto stage_x = [&](int c) {
+    constexpr int PARTS = S::SK * (int)sizeof(typename S::X) / kStepBytes;   // slots of a step
+    static_assert(R % PARTS == 0 && S::XR == 2 * PARTS, "whole steps, two chunks a slot");
+    const int g = lane >> 4, r = lane & 15;
+    const int end = tokens.k * (int)sizeof(typename S::X) - 16;
+#pragma unroll
+    for (int s0 = 0; s0 < NS; s0 += R / PARTS) {
+#pragma unroll
+      for (int q = 0; q < R; ++q) {
+        if (s0 + q / PARTS >= NS) break;
+        const int st = (c * NS + s0 + q / PARTS) * kStreamWaves + wv;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int chunk = (lane & 7) ^ (4 * h | (lane >> 4));
+          const int byte = min((st * PARTS + q % PARTS) * kStepBytes + 16 * chunk, end);
+          load_to_lds(tokens.base, tokens.off[h] + (uint32_t)byte,
+                      ring + q * kStageBytes + h * (kStageBytes / 2));
+        }
+      }
+      wait_loads();
+#pragma unroll
+      for (int q = 0; q < R / PARTS; ++q) {
+        if (s0 + q >= NS) break;
+        const int st = (c * NS + s0 + q) * kStreamWaves + wv;
+#pragma unroll
+        for (int i = 0; i < S::XR; ++i) {
+          const int at = S::XR * g + i;   // 16-byte chunk of the step
+          const u32x4 v = *reinterpret_cast<const u32x4*>(
+              lds.ring[wv][q * PARTS + (PARTS == 1 ? 0 : at >> 3)] + r * kStepBytes +
+              16 * ((at & 7) ^ (r >> 1)));
+          const bool in = st * S::SK + S::k_of(g, i) < tokens.k;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) xs[0][s0 + q][i][e] = in ? v[e] : 0u;
+        }
+      }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // read out before the next loads
     }
+  };
+  const bool restart = FIXED && nchunk > 1;
+  if constexpr (FIXED) {
+    if (!restart) stage_x(0);
+  }
+  if (!restart) fill(0, visits);
   int par = 0;
   for (int v = 0, i = i0; i < i1; ++i) {
     acc = floatx4{0.f, 0.f, 0.f, 0.f};
-    for (int c = 0; c < nchunk; ++c, ++v) {
-      load_x(i, c, xs);
+    if (restart) {
+      if constexpr (FIXED) {
+        for (int c = 0; c < nchunk; ++c, ++v) {
+          stage_x(c);
+          fill(v, 1);
+          visit(std::false_type{}, v);
+        }
+      }
+    } else {
+      if constexpr (!FIXED) load_x(i, xs);
       if (v + AHEAD < visits)
         visit(std::true_type{}, v);
       else
         visit(std::false_type{}, v);
+      ++v;
     }
     red_put(lds.red[par] + wv * kRedWave, acc);
     __syncthreads();
@@ -334,6 +407,26 @@ __device__ __forceinline__ void stream_units(int i0, int i1, int nchunk, int nst
     }
     par ^= 1;
   }
+}
+
+// Calls launch(steps, ring) with the form of stream_units for rows of `per` steps per wave: the
+// least that holds the rows, so that the token operand stays in registers; longer rows run
+// in the chunks that pad them least.  An 8-bit step takes twice the operand's registers.
+template <typename WT, typename Launch>
+void launch_by_steps(int64_t per, Launch launch) {
+#define MOE_STEPS(n, r) launch(std::integral_constant<int, n>{}, std::integral_constant<int, r>{})
+  if (per <= 2) return MOE_STEPS(2, 8);
+  if (per <= 4) return MOE_STEPS(4, 8);
+  if constexpr (sizeof(WT) == 1) {
+    return MOE_STEPS(8, 8);
+  } else {
+    if (per <= 8) return MOE_STEPS(8, 8);
+    if (per <= 14) return MOE_STEPS(14, 7);
+    if (per <= 16) return MOE_STEPS(16, 8);
+    if (per <= 24) return MOE_STEPS(24, 8);
+    return ceil_div(per, 14) * 14 < ceil_div(per, 16) * 16 ? MOE_STEPS(14, 7) : MOE_STEPS(16, 8);
+  }
+#undef MOE_STEPS
 }
 
 }  // namespace moe
