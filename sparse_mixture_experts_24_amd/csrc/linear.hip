@@ -211,10 +211,11 @@ __device__ __forceinline__ void stage_barrier() {
 // 16-byte chunk g of its x row's slice, and the weights of the same k.
 template <typename WT>
 struct Tile {   // bf16
-  static constexpr int BK = 64, WROW = 128;   // k per step, bytes of a weight row in it
+  // k per step, bytes of a weight row in it, MFMAs of a block and slice
+  static constexpr int BK = 64, WROW = 128, SUB = 1;
   typedef bf16_t X;
   typedef u32x4 WReg;
-  __device__ static void mma(floatx4& acc, u32x4 x, u32x4 w) {
+  __device__ static void mma(floatx4& acc, u32x4 x, u32x4 w, int) {
     acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x),
                                                   __builtin_bit_cast(bf16x8, w), acc, 0, 0, 0);
   }
@@ -222,24 +223,24 @@ struct Tile {   // bf16
 };
 template <>
 struct Tile<uint8_t> {
-  static constexpr int BK = 64, WROW = 64;
+  static constexpr int BK = 64, WROW = 64, SUB = 1;
   typedef bf16_t X;
   typedef uint2 WReg;
-  __device__ static void mma(floatx4& acc, u32x4 x, u32x4 w) { Tile<bf16_t>::mma(acc, x, w); }
+  __device__ static void mma(floatx4& acc, u32x4 x, u32x4 w, int) {
+    Tile<bf16_t>::mma(acc, x, w, 0);
+  }
   __device__ static u32x4 operand(uint2 w) {
     return __builtin_bit_cast(u32x4, widen_e4m3(w.x, w.y));
   }
 };
 template <>
 struct Tile<float> {
-  static constexpr int BK = 32, WROW = 128;
+  static constexpr int BK = 32, WROW = 128, SUB = 4;
   typedef float X;
   typedef u32x4 WReg;
-  __device__ static void mma(floatx4& acc, u32x4 x, u32x4 w) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)   // group g holds k = 4 g + j
-      acc = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(x[j]), __uint_as_float(w[j]), acc,
-                                                 0, 0, 0);
+  __device__ static void mma(floatx4& acc, u32x4 x, u32x4 w, int j) {   // group g: k = 4 g + j
+    acc = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(x[j]), __uint_as_float(w[j]), acc,
+                                               0, 0, 0);
   }
   __device__ static u32x4 operand(u32x4 w) { return w; }
 };
@@ -453,40 +454,44 @@ __global__ __launch_bounds__(64 * WM * WN * WK) void linear_tile_kernel(LinearAr
       // between the MFMAs, in whose shadow they issue; so do the loads, of slots in the first
       // half of their slice (LF = 2: gated 4096-row product 760 -> 727 us; whole stages have
       // time to land and prefer an even spread, 213 against 216 us for 2048 x 4096 x 14336).
-      constexpr int B = XB * WB, RD = XB + WB, EVERY = B >= 2 * RD ? 2 : 1, LF = 4;
+      // A block's SUB MFMAs are a round of all blocks apart: each needs the one before.
+      constexpr int SUB = TT::SUB, B = XB * WB * SUB, RD = XB + WB, EVERY = B >= 2 * RD ? 2 : 1,
+                    LF = SLOTS ? 2 : 1;
       static_assert(RD <= B, "a read per MFMA at most");
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int i = 0; i < XB; ++i)
+      for (int u = 0; u < SUB; ++u)
 #pragma unroll
-        for (int j = 0; j < WB; ++j) {
-          const int q = i * WB + j, rd = q / EVERY;
-          TT::mma(acc[i][j], xf[buf][i], wo[j]);
-          if (q % EVERY == 0 && rd < RD) {
-            if (rd < WB)
-              read_w(buf ^ 1, rd < WB ? rd : 0, sw, sn);
-            else
-              read_x(buf ^ 1, rd >= WB ? rd - WB : 0, sx, sn);
-          }
-          if constexpr (decltype(body)::value) {
-            if constexpr (SLOTS) {
-              if (s == 0) {   // x part of step t + 2
+        for (int i = 0; i < XB; ++i)
 #pragma unroll
-                for (int l = q * LF * NX / B; l < min((q + 1) * LF * NX / B, NX); ++l)
-                  load(std::false_type{}, l, t + 2, part_after(nx, 2));
-              } else {
-#pragma unroll
-                for (int l = q * LF * NW / B; l < min((q + 1) * LF * NW / B, NW); ++l)
-                  load(std::false_type{}, NX + l, t + 2, px);
-              }
-            } else if (s == 1) {
-#pragma unroll
-              for (int l = q * LF * L / B; l < min((q + 1) * LF * L / B, L); ++l)
-                load(std::false_type{}, l, t + ST, l < NX ? px : pw);
+          for (int j = 0; j < WB; ++j) {
+            const int q = (u * XB + i) * WB + j, rd = q / EVERY;
+            TT::mma(acc[i][j], xf[buf][i], wo[j], u);
+            if (q % EVERY == 0 && rd < RD) {
+              if (rd < WB)
+                read_w(buf ^ 1, rd < WB ? rd : 0, sw, sn);
+              else
+                read_x(buf ^ 1, rd >= WB ? rd - WB : 0, sx, sn);
             }
+            if constexpr (decltype(body)::value) {
+              if constexpr (SLOTS) {
+                if (s == 0) {   // x part of step t + 2
+#pragma unroll
+                  for (int l = q * LF * NX / B; l < min((q + 1) * LF * NX / B, NX); ++l)
+                    load(std::false_type{}, l, t + 2, part_after(nx, 2));
+                } else {
+#pragma unroll
+                  for (int l = q * LF * NW / B; l < min((q + 1) * LF * NW / B, NW); ++l)
+                    load(std::false_type{}, NX + l, t + 2, px);
+                }
+              } else if (s == 1) {
+#pragma unroll
+                for (int l = q * LF * L / B; l < min((q + 1) * LF * L / B, L); ++l)
+                  load(std::false_type{}, l, t + ST, l < NX ? px : pw);
+              }
+            }
+            __builtin_amdgcn_sched_barrier(0);
           }
-          __builtin_amdgcn_sched_barrier(0);
-        }
       __builtin_amdgcn_sched_barrier(0);
     }
     px = nx;
