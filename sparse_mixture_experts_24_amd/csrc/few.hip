@@ -5,7 +5,19 @@
 // "Mixture-of-experts in practice" (deepseekmodel.com), routing-math and capacity sections.
 //
 // A token chooses an expert at most once, so an expert's rows are a 16-bit set of tokens and
-// the stable rank of an assignment is the number of lower tokens in the set.
+// the stable rank of an assignment is the number of lower tokens in the set: the routing
+// needs no sort, and every workgroup of the first expert kernel forms it for itself.
+//
+// Launches: the logits (routers of more than 16 experts; smaller ones are computed by every
+// workgroup of the next kernel), gate/up with the routing, down in parts of F, the final
+// sums.  Bound by the bytes of the touched experts' weights (16 tokens of a d 4096, d_ff 14336,
+// 8-expert layer: 2.8 GB in 436 us, 6.4 TB/s; gate/up alone 6.5), for one token of a
+// small layer by the launches.  Tried and not kept: everything after the logits in one kernel
+// whose workgroups hand their shares on through memory (one token of the Switch-shaped layer 60
+// to 76 us against 32, the smallest layer 37 us against 16 on the GPU: a hand-over between 256
+// workgroups past the XCDs' L2s costs more than a launch), and the final sums by whichever
+// workgroup finishes a group of columns last (down kernel 149 -> 260 us for 16 tokens: the few
+// that end last do nearly all of it).
 #include <math.h>
 
 #include <algorithm>
@@ -250,7 +262,7 @@ __global__ __launch_bounds__(kFewThreads) void few_logits_kernel(FewArgs a) {
 // h = SiLU(x W_gate^T) * (x W_up^T).  A unit is 8 gate rows and the 8 matching up rows of a
 // touched expert; all T tokens run through it (the matrix cores have the room), and the
 // rows of the tokens that chose the expert are kept.
-template <typename WT, int NS, int R>
+template <typename WT, int NS, int R, bool ENDS>
 __global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(FewArgs a) {
   typedef Stream<WT> S;
   typedef typename S::X XT;
@@ -279,7 +291,7 @@ __global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(FewArgs a) {
   share_of((int64_t)r.nu * upe, blockIdx.x, gridDim.x, i0, i1);
   const int nst = (a.d + S::SK - 1) / S::SK, row_bytes = a.d * (int)sizeof(WT);
   const int nchunk = (nst + NS * kFewWaves - 1) / (NS * kFewWaves);
-  stream_units<WT, NS, R, 1, true>(
+  stream_units<WT, NS, R, 1, true, ENDS>(
       i0, i1, nchunk, nst, row_bytes, lds.stream,
       [&](int i, UnitRows& rows) {
         const int u = i / upe;
@@ -313,7 +325,10 @@ __global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(FewArgs a) {
           } else {
             const bf16_t hi = f32_to_bf16(h);
             ((bf16_t*)a.H)[o] = hi;
-            a.Hlo[o] = f32_to_bf16(h - bf16_to_f32(hi));
+            // infinite (or NaN) values have no remainder
+            a.Hlo[o] = fabsf(h) < INFINITY && (hi & 0x7F80) != 0x7F80
+                           ? f32_to_bf16(h - bf16_to_f32(hi))
+                           : (bf16_t)0;
           }
         }
       });
@@ -322,7 +337,7 @@ __global__ __launch_bounds__(kFewThreads) void few_gate_up_kernel(FewArgs a) {
 // Partial down products: a unit is 16 rows of W_down of an expert over one chunk of F (NS steps
 // per wave); the token operand (the expert's rows of h, in bf16 layers value and remainder)
 // stays in registers over the units of an (expert, chunk).
-template <typename WT, int NS, int R>
+template <typename WT, int NS, int R, bool ENDS>
 __global__ __launch_bounds__(kFewThreads) void few_down_kernel(FewArgs a) {
   typedef Stream<WT> S;
   typedef typename S::X XT;
@@ -337,7 +352,7 @@ __global__ __launch_bounds__(kFewThreads) void few_down_kernel(FewArgs a) {
   int i0, i1, have = -1;
   share_of((int64_t)r.nu * a.chunks * upc, blockIdx.x, gridDim.x, i0, i1);
   const int nst = (a.F + S::SK - 1) / S::SK, row_bytes = a.F * (int)sizeof(WT);
-  stream_units<WT, NS, R, NH, false>(
+  stream_units<WT, NS, R, NH, false, ENDS>(
       i0, i1, 1, nst, row_bytes, lds,
       [&](int i, UnitRows& rows) {
         const int uc = i / upc;
@@ -348,10 +363,10 @@ __global__ __launch_bounds__(kFewThreads) void few_down_kernel(FewArgs a) {
         return uc % a.chunks * NS * kFewWaves;
       },
       [&](int i, u32x4 (&xs)[NH][NS][S::XR]) {
-        const int uc = i / upc;
-        if (uc == have) return;
+        const int uc = i / upc, u = uc / a.chunks, c = uc % a.chunks, t = lane & 15;
+        const int start = c * NS * kFewWaves;
+        if (uc == have) return start;
         have = uc;
-        const int u = uc / a.chunks, c = uc % a.chunks, t = lane & 15;
         const uint32_t mask = r.mask[u];
         const bool mine = (mask >> t) & 1u;
         const int64_t o = (int64_t)(r.row0[u] + __popc(mask & ((1u << t) - 1))) * a.F;
@@ -369,6 +384,7 @@ __global__ __launch_bounds__(kFewThreads) void few_down_kernel(FewArgs a) {
             }
           }
         landed();
+        return start;
       },
       [&](int i, int m, int q, float v) {
         const int uc = i / upc, u = uc / a.chunks, n0 = i % upc * 16;
@@ -392,7 +408,8 @@ __global__ __launch_bounds__(kJoinThreads) void few_join_kernel(FewArgs a) {
   const int64_t i = (int64_t)blockIdx.x * kJoinThreads + threadIdx.x;
   if (i >= (int64_t)a.T * a.d) return;
   const int t = (int)(i / a.d), n = (int)(i % a.d);
-  float y = 0.0f, s = 0.0f, res = 0.0f;
+  float s = 0.0f, res = 0.0f;
+  float y = 0.0f * r.w[t][0];   // NaN where the token's scores were not finite (no experts)
   if (a.residual)
     res = a.out_f32 ? ((const float*)a.residual)[i] : bf16_to_f32(((const bf16_t*)a.residual)[i]);
   for (int j = 0, c = 0; j <= a.k;) {
@@ -440,17 +457,24 @@ struct FewWorkspace {
 // workgroup's routing reads at most 1024 partial sums per token.
 static int64_t logit_parts(const moe_desc_t& d) {
   if (d.n_experts <= kOwnLogits) return 1;
-  const int64_t steps = d.d_model / (d.dtype == MOE_DTYPE_F32 ? Stream<float>::SK : Stream<bf16_t>::SK);
+  const int64_t steps =
+      d.d_model / (d.dtype == MOE_DTYPE_F32 ? Stream<float>::SK : Stream<bf16_t>::SK);
   return std::min(ceil_div(steps, 2 * kFewWaves), std::max<int64_t>(1, 1024 / d.n_experts));
 }
 
-// Elements of F in a chunk of the down products: a wave's NS steps times the waves.
-constexpr int kDownSteps = 4;
+// Steps per wave of a chunk of the down products, and the chunks of F: 4 steps (8 bits: 2, as
+// each takes twice the operand's registers).
+template <typename WT>
+constexpr int down_steps() {
+  return sizeof(WT) == 1 ? 2 : 4;
+}
+template <typename WT>
+static int64_t chunks_of(int64_t F) {
+  return ceil_div(F, (int64_t)Stream<WT>::SK * down_steps<WT>() * kFewWaves);
+}
 static int64_t down_chunks(const moe_desc_t& d, bool fp8) {
-  const int sk = fp8 ? Stream<uint8_t>::SK
-                     : d.dtype == MOE_DTYPE_F32 ? Stream<float>::SK : Stream<bf16_t>::SK;
-  const int ns = fp8 ? kDownSteps / 2 : kDownSteps;
-  return ceil_div(d.d_ff, (int64_t)sk * ns * kFewWaves);
+  if (fp8) return chunks_of<uint8_t>(d.d_ff);
+  return d.dtype == MOE_DTYPE_F32 ? chunks_of<float>(d.d_ff) : chunks_of<bf16_t>(d.d_ff);
 }
 
 static FewWorkspace carve_few(const moe_desc_t& d, void* base) {
@@ -478,24 +502,33 @@ static moe_status_t validate_few(const moe_desc_t* d) {
   return d->T > kFew ? MOE_E_UNSUPPORTED : MOE_OK;
 }
 
-template <typename WT, int NS, int R>
+template <typename WT, int NS, int R, bool ENDS>
 static void launch_gate_up_few(const FewArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL((few_gate_up_kernel<WT, NS, R>), dim3(device_cu_count()), dim3(kFewThreads),
-                     0, s, a);
+  hipLaunchKernelGGL((few_gate_up_kernel<WT, NS, R, ENDS>), dim3(device_cu_count()),
+                     dim3(kFewThreads), 0, s, a);
+}
+template <typename WT, bool ENDS>
+static void launch_down_few(const FewArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL((few_down_kernel<WT, down_steps<WT>(), 8, ENDS>), dim3(device_cu_count()),
+                     dim3(kFewThreads), 0, s, a);
 }
 
 template <typename WT>
 static hipError_t launch_few(const FewArgs& a, hipStream_t s) {
   typedef typename Stream<WT>::X XT;
-  const int per = (int)ceil_div(ceil_div(a.d, Stream<WT>::SK), kFewWaves);   // steps per wave
   if (a.logits)
     hipLaunchKernelGGL(few_logits_kernel<XT>, dim3((unsigned)ceil_div(a.E, 16), a.ks),
                        dim3(kFewThreads), 0, s, a);
-  launch_by_steps<WT>(per, [&](auto steps, auto ring) {
-    launch_gate_up_few<WT, decltype(steps)::value, decltype(ring)::value>(a, s);
+  launch_by_steps<WT>(a.d * (int64_t)sizeof(WT), [&](auto steps, auto ring, auto ends) {
+    launch_gate_up_few<WT, steps.value, ring.value, ends.value>(a, s);
   });
-  hipLaunchKernelGGL((few_down_kernel<WT, sizeof(WT) == 1 ? kDownSteps / 2 : kDownSteps, 8>),
-                     dim3(device_cu_count()), dim3(kFewThreads), 0, s, a);
+  if constexpr (sizeof(WT) == 1) {
+    launch_down_few<WT, false>(a, s);
+  } else if (row_ends<WT>(a.F * (int64_t)sizeof(WT), down_steps<WT>())) {
+    launch_down_few<WT, true>(a, s);
+  } else {
+    launch_down_few<WT, false>(a, s);
+  }
   hipLaunchKernelGGL(few_join_kernel, dim3((unsigned)ceil_div((int64_t)a.T * a.d, kJoinThreads)),
                      dim3(kJoinThreads), 0, s, a);
   return hipGetLastError();

@@ -32,16 +32,17 @@ struct LinearArgs {
 // instructions; the tails keep the sign and never cancel.
 __device__ __forceinline__ float act_f(float z, int act) {
   switch (act) {
-    case MOE_ACT_RELU: return fmaxf(z, 0.0f);
+    case MOE_ACT_RELU: return z < 0.0f ? 0.0f : z;   // NaN stays
     case MOE_ACT_GELU: {
-      const float x = fabsf(z) * 0.70710678118654752f;
+      const float y = __builtin_amdgcn_fmed3f(z, -16.0f, 16.0f);   // the tail of more is zero
+      const float x = fabsf(y) * 0.70710678118654752f;
       const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f, x, 1.0f));
       float p = fmaf(1.061405429f, t, -1.453152027f);
       p = fmaf(p, t, 1.421413741f);
       p = fmaf(p, t, -0.284496736f);
       p = fmaf(p, t, 0.254829592f);
-      const float tail = 0.5f * z * (p * t) * __expf(-x * x);   // z/2 erfc(x)
-      return z >= 0.0f ? z - tail : tail;
+      const float tail = 0.5f * y * (p * t) * __expf(-x * x);   // z/2 erfc(x)
+      return z < 0.0f ? tail : z - tail;                        // NaN stays
     }
     case MOE_ACT_GELU_TANH:
       return z * __builtin_amdgcn_rcpf(
@@ -128,8 +129,11 @@ __device__ __forceinline__ void store8(const LinearArgs& a, int64_t i, const flo
 }
 
 // ------------------------------------------------------------------ at most 16 rows
-// A unit is 16 weight rows (gated: 8 gate rows and the 8 matching up rows).
-template <typename WT, int NS, int R, bool GATED>
+// Bound by the weights' bytes, or for small ones by a launch and two trips to memory: one row
+// of 2048 x 2048 3.9 us, 16 rows against 2 x 14336 x 4096 of 8 bits 24 us a call (4.8 TB/s).  A
+// unit is 16 weight rows (gated: 8 gate rows and the 8 matching up rows); workgroups take
+// runs of units.
+template <typename WT, int NS, int R, bool ENDS, bool GATED>
 __global__ __launch_bounds__(kStreamThreads) void linear_rows_kernel(LinearArgs a) {
   typedef Stream<WT> S;
   typedef typename S::X XT;
@@ -141,7 +145,7 @@ __global__ __launch_bounds__(kStreamThreads) void linear_rows_kernel(LinearArgs 
   const int nst = (a.K + S::SK - 1) / S::SK;
   const int nchunk = (nst + NS * kStreamWaves - 1) / (NS * kStreamWaves);
   const uint32_t wrow = (uint32_t)(a.ldw * (int)sizeof(WT));
-  stream_units<WT, NS, R, 1, true>(
+  stream_units<WT, NS, R, 1, true, ENDS>(
       i0, i1, nchunk, nst, a.K * (int)sizeof(WT), lds,
       [&](int i, UnitRows& rows) {
 #pragma unroll
@@ -157,7 +161,8 @@ __global__ __launch_bounds__(kStreamThreads) void linear_rows_kernel(LinearArgs 
         x.k = a.K;
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          x.off[h] = (uint32_t)min(8 * h + (lane >> 3), a.M - 1) * (uint32_t)(a.ldx * (int)sizeof(XT));
+          x.off[h] = (uint32_t)min(8 * h + (lane >> 3), a.M - 1) *
+                     (uint32_t)(a.ldx * (int)sizeof(XT));
       },
       [&](int i, int m, int q, float v) {
         const int n0 = i * COLS, n = n0 + (GATED ? q & 7 : q);
@@ -185,8 +190,10 @@ __global__ __launch_bounds__(kStreamThreads) void linear_rows_kernel(LinearArgs 
 // ------------------------------------------------------------------ MFMA tiles
 // A tile per workgroup of WM x WN waves, a wave holding MB x NB blocks of 32 x 32 sums (each
 // four MFMAs of 16 x 16: the 32 x 32 MFMA moves twice the sums through the registers per
-// product, and large products run at the clock that the card's power allows).  K runs in steps of 128 bytes of an x row through ST LDS stages that global loads fill
-// directly (no registers between).  A step is two slices of one k range per MFMA block; the
+// product, and large products run at the clock that the card's power allows: 1.44 GHz and
+// 82% of it in MFMAs with the one, 1.62 GHz and 75% with the other).  K runs in steps of
+// 128 bytes of an x row through ST LDS stages that global loads fill directly (no registers
+// between).  A step is two slices of one k range per MFMA block; the
 // operands of slice s + 1 are read from LDS while the MFMAs of slice s run.  The barrier that
 // frees a stage stands before the last slice's MFMAs, whose operands are in registers by
 // then, so the next stage's first reads and the loads ST steps ahead run under them.
@@ -199,8 +206,13 @@ __global__ __launch_bounds__(kStreamThreads) void linear_rows_kernel(LinearArgs 
 // rows then cover 256 bytes, all 64 banks.
 //   Small products have less than a tile for every CU: there WK groups of waves with stages of
 // their own take every WK-th step and their sums are added through LDS.
-//   Gated: the weight blocks of a wave alternate gate and up rows of the same columns, so
-// act(g) * u is formed in registers.
+//   Gated: the weight blocks of a wave alternate gate and up rows of the same columns, so the
+// two sums of an output meet in the epilogue's buffer.
+//   Bound: MFMAs at the power limit for large products (gated 4096 x 14336 x 4096: 694 us, 1390
+// TFLOP/s; the library's plain product of the same size 630-710 us; 2048 x 4096 x 14336 with
+// the residual 216 us, 1110 TFLOP/s), the loads of a CU for small ones (64 x 7168 x 2048:
+// 8.1 us with its inputs in the caches, 64 x 14336 x 4096 21 us against the library's 24).
+
 // Barrier that LDS accesses do not cross.
 __device__ __forceinline__ void stage_barrier() {
   __builtin_amdgcn_s_barrier();
@@ -318,7 +330,8 @@ __global__ __launch_bounds__(64 * WM * WN * WK) void linear_tile_kernel(LinearAr
   // What this lane loads: rows of the tile (clamped into the matrices) at its chunk, as 32-bit
   // offsets from the tile's first rows (the host keeps tiles within 4 GB of them).  Load i of
   // x takes 8 rows, chunk lane % 8 ^ row / 2 % 8, whose third bit is the parity of i.
-  const uint32_t xrow = (uint32_t)(a.ldx * (int)sizeof(XT)), wrow = (uint32_t)(a.ldw * (int)sizeof(WT));
+  const uint32_t xrow = (uint32_t)(a.ldx * (int)sizeof(XT));
+  const uint32_t wrow = (uint32_t)(a.ldw * (int)sizeof(WT));
   const int xchunk = (lane & 7) ^ (lane >> 4);
   const int wchunk = W8 ? (lane & 3) ^ ((lane >> 4) & 3) : xchunk;
   uint32_t ox[NX], ow[NW];
@@ -388,11 +401,13 @@ __global__ __launch_bounds__(64 * WM * WN * WK) void linear_tile_kernel(LinearAr
   u32x4 xf[2][XB];
   typename TT::WReg wf[2][WB];
   auto read_x = [&](int buf, int i, int part, int s) {
-    xf[buf][i] = *reinterpret_cast<const u32x4*>(smem + part + xrd + i * 16 * kXRow + (xsw ^ (64 * s)));
+    xf[buf][i] = *reinterpret_cast<const u32x4*>(smem + part + xrd + i * 16 * kXRow +
+                                                 (xsw ^ (64 * s)));
   };
   auto read_w = [&](int buf, int i, int part, int s) {
     wf[buf][i] = *reinterpret_cast<const typename TT::WReg*>(
-        smem + part + wrd + i * 16 * TT::WROW + (W8 ? (wsw ^ (32 * s)) + 8 * (fg & 1) : wsw ^ (64 * s)));
+        smem + part + wrd + i * 16 * TT::WROW +
+        (W8 ? (wsw ^ (32 * s)) + 8 * (fg & 1) : wsw ^ (64 * s)));
   };
   floatx4 acc[XB][WB];
 #pragma unroll
@@ -613,10 +628,10 @@ static hipError_t run_tiles(const LinearArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <typename WT, int NS, int R, bool GATED>
+template <typename WT, int NS, int R, bool ENDS, bool GATED>
 static hipError_t run_rows(const LinearArgs& a, hipStream_t s) {
   const int64_t units = ceil_div(a.N, GATED ? 8 : 16);
-  hipLaunchKernelGGL((linear_rows_kernel<WT, NS, R, GATED>),
+  hipLaunchKernelGGL((linear_rows_kernel<WT, NS, R, ENDS, GATED>),
                      dim3((unsigned)std::min<int64_t>(units, device_cu_count())),
                      dim3(kStreamThreads), 0, s, a);
   return hipGetLastError();
@@ -625,8 +640,8 @@ static hipError_t run_rows(const LinearArgs& a, hipStream_t s) {
 template <typename WT, bool GATED>
 static hipError_t launch_rows(const LinearArgs& a, hipStream_t s) {
   hipError_t e = hipSuccess;
-  launch_by_steps<WT>(ceil_div(ceil_div(a.K, Stream<WT>::SK), kStreamWaves), [&](auto steps, auto ring) {
-    e = run_rows<WT, decltype(steps)::value, decltype(ring)::value, GATED>(a, s);
+  launch_by_steps<WT>(a.K * (int64_t)sizeof(WT), [&](auto steps, auto ring, auto ends) {
+    e = run_rows<WT, steps.value, ring.value, ends.value, GATED>(a, s);
   });
   return e;
 }
@@ -644,7 +659,8 @@ static hipError_t launch_linear_t(const LinearArgs& a, hipStream_t s) {
   constexpr int out = GATED ? 2 : 1;   // weight rows per output column
   typedef Tile<WT> TT;
   const int64_t cus = device_cu_count(), steps = ceil_div(a.K, TT::BK);
-  const int64_t row = std::max(a.ldx * (int64_t)sizeof(typename TT::X), a.ldw * (int64_t)sizeof(WT));
+  const int64_t row =
+      std::max(a.ldx * (int64_t)sizeof(typename TT::X), a.ldw * (int64_t)sizeof(WT));
   const bool near_rows = row * 256 < ((int64_t)1 << 32);   // for tiles taller than 64
   // per: products that a CU does in a clock on such a tile, as measured in bf16
   auto clocks = [&](int m, int w, double per) -> double {
@@ -654,11 +670,16 @@ static hipError_t launch_linear_t(const LinearArgs& a, hipStream_t s) {
     const double tile = steps * std::max(loads, mma) + 4000.0 + m * (double)w / 4.0;
     return (double)ceil_div(ceil_div(a.M, m) * ceil_div(a.N * (int64_t)out, w), cus) * tile;
   };
-  const double t[] = {clocks(256, 256, 1536),     clocks(256, 128, 1280),
-                      clocks(128, 128, 1024),     clocks(64, 64 * out, 1024),
-                      clocks(64, 32 * out, 1024), clocks(32, 32 * out, 1024)};
+  // float MFMAs bound every tile alike, and the registers of 256 x 256 spill (4096 x 4096 x
+  // 4096 in 940 us, 919 without it)
+  constexpr bool LARGE = sizeof(WT) != 4;
+  const double t[] = {LARGE ? clocks(256, 256, 1536) : 1e300, clocks(256, 128, 1280),
+                      clocks(128, 128, 1024),                 clocks(64, 64 * out, 1024),
+                      clocks(64, 32 * out, 1024),             clocks(32, 32 * out, 1024)};
   switch ((int)(std::min_element(t, t + 6) - t)) {
-    case 0: return run_tiles<WT, 4, 2, 2, 4, 1, 2, GATED>(a, s);
+    case 0:
+      if constexpr (LARGE) return run_tiles<WT, 4, 2, 2, 4, 1, 2, GATED>(a, s);
+      [[fallthrough]];
     case 1: return run_tiles<WT, 2, 2, 4, 2, 1, 3, GATED>(a, s);
     case 2: return run_tiles<WT, 1, 2, 4, 2, 1, 4, GATED>(a, s);
     case 3: return run_tiles<WT, 1, out, 2, 2, 1, GATED ? 3 : 4, GATED>(a, s);

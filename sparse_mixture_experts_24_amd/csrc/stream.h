@@ -224,6 +224,7 @@ __device__ __forceinline__ float pick(const float* p, int64_t i, int q) {
   for (int j = 1; j < N; ++j) v = q == j ? s[j] : v;
   return v;
 }
+
 // Where the rows of a unit are: load h takes row h * 8 + lane / 8 at base[h] + off[h].
 struct UnitRows {
   const char* base[2];   // uniform
@@ -251,14 +252,15 @@ struct TokenRows {
 //                        chunk every visit starts over, tokens first.
 //                        Else: load_x(i, xs) loads the wave's operand for unit i (or leaves
 //                        it as it is), xs[0 .. NH - 1] multiplied by the same weights, zero
-//                        past the rows' end, and ends with landed(); one chunk only
+//                        past the rows' end, ends with landed() and returns the unit's
+//                        first step; one chunk only
 //   done(i, m, n, v)     sum v of token m and weight row n of the unit, called by 256 threads
 //                        (whole waves); a vector load there empties the ring
 //   nst, row_bytes       steps and bytes of a weight row
 // Steps past nst repeat its last one and bytes past the row its last chunk (cache hits); the
-// token operand is zero there.
-template <typename WT, int NS, int R, int NH, bool FIXED, typename Point, typename LoadX,
-          typename Done>
+// token operand is zero there, and with ENDS the weights, which may be infinite, as well.
+template <typename WT, int NS, int R, int NH, bool FIXED, bool ENDS, typename Point,
+          typename LoadX, typename Done>
 __device__ __forceinline__ void stream_units(int i0, int i1, int nchunk, int nst, int row_bytes,
                                              StreamLds<R>& lds, Point point, LoadX load_x,
                                              Done done) {
@@ -284,21 +286,21 @@ __device__ __forceinline__ void stream_units(int i0, int i1, int nchunk, int nst
     for (int h = 0; h < 2; ++h) {
       const int chunk = (lane & 7) ^ (4 * h | (lane >> 4));
       const int byte = min(st * kStepBytes + 16 * chunk, row_bytes - 16);
-      load_to_lds<true>(rows.base[h], rows.off[h] + (uint32_t)byte, ring + slot + h * (kStageBytes / 2));
+      load_to_lds<true>(rows.base[h], rows.off[h] + (uint32_t)byte,
+                        ring + slot + h * (kStageBytes / 2));
     }
   };
   floatx4 acc;
   uint32_t slot = 0;   // of the step in use, bytes from ring
-  // Visit v; more: the steps R further exist for all of its steps.
-  auto visit = [&](auto more, int v) {
+  // Visit v, whose first step is `start`; more: the steps R further exist for all its steps.
+  auto visit = [&](auto more, int v, int start) {
     if (AHEAD > 1 || R == NS) {
       if constexpr (decltype(more)::value) point_at(v + AHEAD);
     }
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
       // steps that may still be under way when this one is needed
-      constexpr int rest_max = R - 1;
-      const int rest = decltype(more)::value ? rest_max : (NS - 1 - s < rest_max ? NS - 1 - s : rest_max);
+      const int rest = decltype(more)::value || NS - s > R ? R - 1 : NS - 1 - s;
       switch (rest) {   // a constant once unrolled
 #define MOE_WAIT(n) case n: wait_loads<2 * n>(); break;
         MOE_WAIT(0) MOE_WAIT(1) MOE_WAIT(2) MOE_WAIT(3) MOE_WAIT(4) MOE_WAIT(5) MOE_WAIT(6)
@@ -309,6 +311,14 @@ __device__ __forceinline__ void stream_units(int i0, int i1, int nchunk, int nst
       stage_out(lds.ring[wv][0] + slot, lane, w0, w1);
       // the slot is read out before it is filled again
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      if constexpr (ENDS) {
+        const int left = row_bytes - (start + s * kStreamWaves + wv) * kStepBytes;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {   // no branch: it would spill the 24-step form in float
+          w0[e] = 32 * (lane >> 4) < left ? w0[e] : 0u;
+          w1[e] = 32 * (lane >> 4) + 16 < left ? w1[e] : 0u;
+        }
+      }
       if (s + R < NS) {
         load(s + R, slot);
       } else if constexpr (decltype(more)::value) {
@@ -386,15 +396,16 @@ __device__ __forceinline__ void stream_units(int i0, int i1, int nchunk, int nst
         for (int c = 0; c < nchunk; ++c, ++v) {
           stage_x(c);
           fill(v, 1);
-          visit(std::false_type{}, v);
+          visit(std::false_type{}, v, c * NS * kStreamWaves);
         }
       }
     } else {
-      if constexpr (!FIXED) load_x(i, xs);
+      int start = 0;
+      if constexpr (!FIXED) start = __builtin_amdgcn_readfirstlane(load_x(i, xs));
       if (v + AHEAD < visits)
-        visit(std::true_type{}, v);
+        visit(std::true_type{}, v, start);
       else
-        visit(std::false_type{}, v);
+        visit(std::false_type{}, v, start);
       ++v;
     }
     red_put(lds.red[par] + wv * kRedWave, acc);
@@ -409,12 +420,28 @@ __device__ __forceinline__ void stream_units(int i0, int i1, int nchunk, int nst
   }
 }
 
-// Calls launch(steps, ring) with the form of stream_units for rows of `per` steps per wave: the
-// least that holds the rows, so that the token operand stays in registers; longer rows run
-// in the chunks that pad them least.  An 8-bit step takes twice the operand's registers.
+// Whether rows of row_bytes end inside the NS x 8 steps of a visit.  A form of its own: masking
+// costs 10% of float rows (14.8 -> 16.4 us for 16 x 4096 x 4096).  8-bit weights have no
+// infinities and need none.
+template <typename WT>
+bool row_ends(int64_t row_bytes, int ns) {
+  return sizeof(WT) > 1 && row_bytes % ((int64_t)ns * kStreamWaves * kStepBytes) != 0;
+}
+
+// Calls launch(steps, ring, ends) with the form of stream_units for rows of row_bytes: the least
+// number of steps per wave that holds the rows, so that the token operand stays in registers;
+// longer rows run in the chunks that pad them least.  An 8-bit step takes twice the
+// operand's registers.
 template <typename WT, typename Launch>
-void launch_by_steps(int64_t per, Launch launch) {
-#define MOE_STEPS(n, r) launch(std::integral_constant<int, n>{}, std::integral_constant<int, r>{})
+void launch_by_steps(int64_t row_bytes, Launch launch) {
+  const int64_t per = ceil_div(row_bytes, (int64_t)kStreamWaves * kStepBytes);
+  auto run = [&](auto steps, auto ring) {
+    if constexpr (sizeof(WT) > 1) {
+      if (row_ends<WT>(row_bytes, steps.value)) return launch(steps, ring, std::true_type{});
+    }
+    launch(steps, ring, std::false_type{});
+  };
+#define MOE_STEPS(n, r) run(std::integral_constant<int, n>{}, std::integral_constant<int, r>{})
   if (per <= 2) return MOE_STEPS(2, 8);
   if (per <= 4) return MOE_STEPS(4, 8);
   if constexpr (sizeof(WT) == 1) {

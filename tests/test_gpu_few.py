@@ -231,6 +231,43 @@ def test_residual_in_place_and_no_statistics():
     assert f is None and p is None
 
 
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_infinite_and_nan_values(kind):
+    """A token with a NaN is NaN and the others are as before; an infinite weight gives the
+    formula's infinities to the tokens of its expert, also at the end of a row that ends
+    inside a step."""
+    c = make(T=6, d=192, E=4, k=2, F=1216, kind=kind, residual=True, out=F32, seed=12)
+    y, _, _ = call(c)
+    _, _, _, _, kept = reference(c)
+    bad = dict(c, x=c["x"].clone())
+    bad["x"][2, 100] = math.nan
+    got, _, _ = call(bad)
+    rest = [0, 1, 3, 4, 5]
+    assert torch.isnan(got[2]).all() and torch.equal(got[rest], y[rest])
+    e = max(kept, key=lambda q: len(kept[q]))
+    mine = [t in kept[e] for t in range(6)]
+    assert any(mine) and not all(mine)
+    other = [t for t in range(6) if not mine[t]]
+    # W_down[e, 7, last]: output 7 of the expert's tokens, the sign that of h
+    down = c["w"][2].clone()
+    down[e, 7, -1] = math.inf
+    got, _, _ = call(dict(c, w=[c["w"][0], c["w"][1], down]))
+    x = c["x"].double()
+    g, u = x @ c["w"][0][e, -1].double(), x @ c["w"][1][e, -1].double()
+    want = y.clone()
+    want[mine, 7] = torch.sign(g * u)[mine].float() * math.inf
+    assert torch.equal(got, want)
+    # W_up[e, 3, last]: h[3] is infinite, and every output of the expert's tokens with it
+    up = c["w"][1].clone()
+    up[e, 3, -1] = math.inf
+    got, _, _ = call(dict(c, w=[c["w"][0], up, c["w"][2]]))
+    h = torch.sign(c["x"][:, -1].double() * (x @ c["w"][0][e, 3].double()))
+    sign = h[:, None] * torch.sign(c["w"][2][e, :, 3].double())[None, :]
+    assert (sign != 0).all()
+    assert torch.equal(got[mine], (sign[mine] * math.inf).float())
+    assert torch.equal(got[other], y[other])
+
+
 def test_no_tokens():
     c = make(T=0, d=128, E=4, k=2, F=64, S=1)
     y, f, p = call(c)

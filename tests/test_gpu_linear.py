@@ -220,3 +220,35 @@ def test_offsets_past_32_bits():
     for rows in (M, 3):
         got = moe.linear(x[-rows:], W, out=out[-rows:])
         check(got, *reference(x[-rows:], [W.double()], [None], None, "none"))
+
+
+@pytest.mark.parametrize("M,N,K,kind", [(1, 70, 2056, "bf16"), (3, 70, 36, "f32"),
+                                        (16, 200, 13320, "bf16"), (16, 70, 4108, "f32"),
+                                        (40, 70, 520, "bf16"), (40, 70, 44, "f32"),
+                                        (300, 260, 8200, "bf16"), (300, 260, 1100, "f32")])
+@pytest.mark.parametrize("act", list(moe.ACTS))
+def test_infinite_and_nan_values(M, N, K, kind, act):
+    """Rows and columns that hold infinities or NaN give what the formula gives, also where K
+    ends inside a step, and leave the others alone."""
+    x, ws, ss, wide, bs, r = make(M, N, K, kind, False, True, True, F32, 17)
+    x.abs_().add_(0.5)
+    W = ws[0]
+    W[1, K - 1] = math.inf      # z = +inf
+    W[2, K // 2] = math.nan
+    if act in ("none", "relu"):
+        W[5, K - 1] = -math.inf
+    if M > 2:
+        x[1, K - 1] = math.nan
+    got = moe.linear(x, W, bs[0], act=act, residual=r, out_dtype=F32)
+    y, dy = reference(x.nan_to_num(0.0), [W.double().nan_to_num(0.0, 0.0, 0.0)], bs, r, act)
+    y[:, 1] = math.inf          # every activation of +inf
+    if act in ("none", "relu"):
+        y[:, 5] = -math.inf if act == "none" else r[:, 5].double()
+    y[:, 2] = math.nan
+    if M > 2:
+        y[1] = math.nan
+    assert torch.equal(torch.isnan(got), torch.isnan(y))
+    inf = torch.isinf(y)
+    assert inf.any() and torch.equal(got[inf].double(), y[inf])
+    ok = torch.isfinite(y)
+    check(got[ok], y[ok], dy[ok])
