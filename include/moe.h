@@ -315,7 +315,8 @@ moe_status_t moe_forward_noalloc(const moe_desc_t* desc, const void* x, const vo
  * Sums, bias, activation and residual are 32-bit; the one rounding is out's.
  * The rows of x, W, residual and out may be strided (elements from row to row; 0: packed).
  * residual may be out itself (same stride); out must not overlap any other argument.
- * M == 0 enqueues nothing.  Every other convention is that of the entry points above. */
+ * Infinities and NaN give what the formula gives, and only in the rows and columns that hold
+ * them.  M == 0 enqueues nothing.  Every other convention is that of the entry points above. */
 typedef enum {
   MOE_ACT_NONE = 0,
   MOE_ACT_RELU = 1,       /* max(z, 0) */
@@ -363,7 +364,9 @@ moe_status_t moe_linear_gated_fp8(const moe_linear_desc_t* desc, const void* x,
  * Same layer, layouts and rules as moe_forward (capacity and shared expert included); h is
  * carried with the precision of float32 sums, not rounded to bf16, so outputs are at least
  * as exact as moe_forward's and may differ from them by that rounding.  Without a capacity
- * a token's output does not depend on the other tokens of the call.  residual may be out.
+ * a token's output does not depend on the other tokens of the call; a token whose scores are
+ * not finite takes no expert's capacity and has NaN in out (and makes p NaN).  residual may be
+ * out, and out may be x.  x, the weights, residual and out are 16-byte aligned.
  * T > MOE_FEW_TOKENS is MOE_E_UNSUPPORTED.  The workspace (256-byte aligned, contents
  * arbitrary) comes from moe_workspace_bytes_few (0 for an invalid description). */
 #define MOE_FEW_TOKENS 16
