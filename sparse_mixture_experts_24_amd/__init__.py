@@ -718,8 +718,10 @@ def _few(name, x, W_router, bias, weights, scales, k, capacity_factor, residual,
             p = torch.empty(E, dtype=torch.float32, device=dev)
     if workspace is None:
         workspace = alloc_workspace_few(desc, dev)
+    else:
+        _require(workspace, "workspace", dev)
     args += [_opt_ptr(residual), out.data_ptr(), _opt_ptr(f), _opt_ptr(p), workspace.data_ptr(),
-             workspace.numel(), _raw_stream(dev)]
+             workspace.numel() * workspace.element_size(), _raw_stream(dev)]
     _check(name, getattr(lib(), name)(desc, *args))
     return out, f, p
 

@@ -274,6 +274,20 @@ def test_no_tokens():
     assert y.shape == (0, 128) and float(f.abs().sum() + p.abs().sum()) == 0.0
 
 
+def test_workspaces_that_are_refused():
+    """On the host, scattered, too small: an error, and no launch."""
+    c = make(T=2, d=128, E=4, k=2, F=64, seed=13)
+    n = moe.workspace_bytes_few(moe.make_desc(2, 128, 4, 64, 2, 0))
+    with pytest.raises(ValueError, match="workspace"):
+        call(c, workspace=torch.empty(n, dtype=torch.uint8))
+    with pytest.raises(ValueError, match="workspace"):
+        call(c, workspace=torch.empty(2 * n, dtype=torch.uint8, device=DEV)[::2])
+    with pytest.raises(moe.MoeError):
+        call(c, workspace=torch.empty(n - 1, dtype=torch.uint8, device=DEV))
+    y, _, _ = call(c, workspace=torch.empty(-(-n // 4), dtype=F32, device=DEV))
+    assert torch.equal(y, call(c)[0])
+
+
 def test_one_workspace_for_any_number_of_tokens():
     """Workspace contents are arbitrary: filled with ones, then reused by smaller and larger
     calls one after the other."""
