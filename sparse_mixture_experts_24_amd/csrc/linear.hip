@@ -128,11 +128,11 @@ __device__ __forceinline__ void store8(const LinearArgs& a, int64_t i, const flo
   }
 }
 
-// ------------------------------------------------------------------ at most 16 rows
+// ------------------------------------------------------------------ blocks of 16 rows
 // Bound by the weights' bytes, or for small ones by a launch and two trips to memory: one row
 // of 2048 x 2048 3.9 us, 16 rows against 2 x 14336 x 4096 of 8 bits 24 us a call (4.8 TB/s).  A
-// unit is 16 weight rows (gated: 8 gate rows and the 8 matching up rows); workgroups take
-// runs of units.
+// unit is 16 weight rows (gated: 8 gate rows and the 8 matching up rows); the workgroups of
+// a row block take runs of units.
 template <typename WT, int NS, int R, bool ENDS, bool GATED>
 __global__ __launch_bounds__(kStreamThreads) void linear_rows_kernel(LinearArgs a) {
   typedef Stream<WT> S;
@@ -140,6 +140,9 @@ __global__ __launch_bounds__(kStreamThreads) void linear_rows_kernel(LinearArgs 
   __shared__ StreamLds<R> lds;
   constexpr int COLS = GATED ? 8 : 16;   // output columns of a unit
   const int lane = threadIdx.x & 63;
+  const int m0 = blockIdx.y * 16;   // the block's rows
+  a.x = (const XT*)a.x + m0 * a.ldx;
+  a.M = min(a.M - m0, 16);
   int i0, i1;
   share_of((a.N + COLS - 1) / COLS, blockIdx.x, gridDim.x, i0, i1);
   const int nst = (a.K + S::SK - 1) / S::SK;
@@ -182,8 +185,8 @@ __global__ __launch_bounds__(kStreamThreads) void linear_rows_kernel(LinearArgs 
           v = act_f(z[0], a.act);
         }
         if (m >= a.M || n >= a.N) return;
-        if (a.residual) v += load_out(a, a.residual, m * a.ldr + n);
-        store_out(a, m * a.ldo + n, v);
+        if (a.residual) v += load_out(a, a.residual, (m0 + m) * a.ldr + n);
+        store_out(a, (m0 + m) * a.ldo + n, v);
       });
 }
 
@@ -630,9 +633,10 @@ static hipError_t run_tiles(const LinearArgs& a, hipStream_t s) {
 
 template <typename WT, int NS, int R, bool ENDS, bool GATED>
 static hipError_t run_rows(const LinearArgs& a, hipStream_t s) {
-  const int64_t units = ceil_div(a.N, GATED ? 8 : 16);
+  const int64_t units = ceil_div(a.N, GATED ? 8 : 16), blocks = ceil_div(a.M, 16);
+  const int64_t per = std::max<int64_t>(1, device_cu_count() / blocks);
   hipLaunchKernelGGL((linear_rows_kernel<WT, NS, R, ENDS, GATED>),
-                     dim3((unsigned)std::min<int64_t>(units, device_cu_count())),
+                     dim3((unsigned)std::min(units, per), (unsigned)blocks),
                      dim3(kStreamThreads), 0, s, a);
   return hipGetLastError();
 }
@@ -680,7 +684,19 @@ static hipError_t launch_linear_t(const LinearArgs& a, hipStream_t s) {
   const double t[] = {LARGE ? clocks(256, 256, 1536) : 1e300, clocks(256, 128, 1280),
                       clocks(128, 128, 1024),                 clocks(64, 64 * out, 1024),
                       clocks(64, 32 * out, 1024),             clocks(32, 32 * out, 1024)};
-  switch ((int)(std::min_element(t, t + 6) - t)) {
+  // Blocks of 16 rows as weight streams: the most workgroups for a product of few tiles and
+  // the whole of a CU for each, a later start (gated float 83 x 70 x 5488 in 32 x 32 tiles 46
+  // us, in 16-row blocks 19; bf16 15 and 8.5; but bf16 64 x 1000 x 2048 6.8 and 7.9).
+  const int64_t blocks = ceil_div(a.M, 16), units = ceil_div(a.N * (int64_t)out, 16);
+  const int64_t per = std::min(units, std::max<int64_t>(1, cus / blocks));
+  const double step = 16 * (kXRow + TT::WROW) / 34.0;
+  // long rows: the token rows again for every unit
+  const bool again = units > per && rows_in_chunks<WT>(a.K * (int64_t)sizeof(WT));
+  const int64_t runs = ceil_div(units, per) * ceil_div(blocks * per, cus);
+  const double rows = (double)(runs * steps) * step * (again ? 1.5 : 1.0) + 8000.0;
+  const double* best = std::min_element(t, t + 6);
+  if (rows < *best) return launch_rows<WT, GATED>(a, s);
+  switch ((int)(best - t)) {
     case 0:
       if constexpr (LARGE) return run_tiles<WT, 4, 2, 2, 4, 1, 2, GATED>(a, s);
       [[fallthrough]];

@@ -428,6 +428,12 @@ bool row_ends(int64_t row_bytes, int ns) {
   return sizeof(WT) > 1 && row_bytes % ((int64_t)ns * kStreamWaves * kStepBytes) != 0;
 }
 
+// Whether launch_by_steps runs rows of row_bytes in several chunks.
+template <typename WT>
+bool rows_in_chunks(int64_t row_bytes) {
+  return row_bytes > (sizeof(WT) == 1 ? 8 : 24) * (int64_t)kStreamWaves * kStepBytes;
+}
+
 // Calls launch(steps, ring, ends) with the form of stream_units for rows of row_bytes: the least
 // number of steps per wave that holds the rows, so that the token operand stays in registers;
 // longer rows run in the chunks that pad them least.  An 8-bit step takes twice the

@@ -157,6 +157,20 @@ def test_strided_rows(M, N, K, kind):
     assert bool((buf[:, N:] == -3.0).all())
 
 
+@pytest.mark.parametrize("M,N,K", [(17, 20, 8208), (33, 130, 2064), (83, 70, 5488),
+                                   (320, 98, 5632), (40, 33, 16400)])
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "f32"])
+@pytest.mark.parametrize("gated", [False, True])
+def test_few_columns_and_long_rows(M, N, K, kind, gated):
+    """More than 16 rows, too few tiles for the GPU: rows go through in blocks of 16."""
+    x, ws, ss, wide, bs, r = make(M, N, K, kind, gated, True, True, F32, 23, ldx=K + 64,
+                                  ldw=K + 32, ldr=N + 4)
+    y, dy = reference(x, wide, bs, r, "silu")
+    got = call(x, ws, ss, bs, r, "silu", out_dtype=F32)
+    check(got, y, dy, f"{M} {N} {K}")
+    assert torch.equal(got, call(x, ws, ss, bs, r, "silu", out_dtype=F32))
+
+
 @pytest.mark.parametrize("M,N,K", [(1, 2048, 2048), (16, 512, 4096), (300, 256, 512)])
 def test_in_place_residual_and_determinism(M, N, K):
     print(f"\n[linear] in place {M}x{N}x{K}", flush=True)
