@@ -140,7 +140,10 @@ __global__ __launch_bounds__(kStreamThreads) void linear_rows_kernel(LinearArgs 
   __shared__ StreamLds<R> lds;
   constexpr int COLS = GATED ? 8 : 16;   // output columns of a unit
   const int lane = threadIdx.x & 63;
-  const int m0 = blockIdx.y * 16;   // the block's rows
+  // The block's rows.  Neighbouring workgroups are of one block: the blocks' workgroups of the
+  // same weight rows are then often on one XCD, whose L2 they share (float32 24 x 4096 x 4096
+  // 19 us, 25 in the other order).
+  const int m0 = blockIdx.y * 16;
   a.x = (const XT*)a.x + m0 * a.ldx;
   a.M = min(a.M - m0, 16);
   int i0, i1;
@@ -650,6 +653,8 @@ static hipError_t launch_rows(const LinearArgs& a, hipStream_t s) {
   return e;
 }
 
+constexpr int64_t kMaxGridY = 65535;
+
 template <typename WT, bool GATED>
 static hipError_t launch_linear_t(const LinearArgs& a, hipStream_t s) {
   if (a.M <= 16) return launch_rows<WT, GATED>(a, s);
@@ -692,10 +697,10 @@ static hipError_t launch_linear_t(const LinearArgs& a, hipStream_t s) {
   const double step = 16 * (kXRow + TT::WROW) / 34.0;
   // long rows: the token rows again for every unit
   const bool again = units > per && rows_in_chunks<WT>(a.K * (int64_t)sizeof(WT));
-  const int64_t runs = ceil_div(units, per) * ceil_div(blocks * per, cus);
-  const double rows = (double)(runs * steps) * step * (again ? 1.5 : 1.0) + 8000.0;
+  const double run = (double)(ceil_div(units, per) * steps) * step * (again ? 1.5 : 1.0);
+  const double rows = (double)ceil_div(blocks * per, cus) * (run + 8000.0);
   const double* best = std::min_element(t, t + 6);
-  if (rows < *best) return launch_rows<WT, GATED>(a, s);
+  if (blocks <= kMaxGridY && rows < *best) return launch_rows<WT, GATED>(a, s);
   switch ((int)(best - t)) {
     case 0:
       if constexpr (LARGE) return run_tiles<WT, 4, 2, 2, 4, 1, 2, GATED>(a, s);

@@ -216,6 +216,21 @@ def test_graph_replays_and_two_streams(M):
         assert torch.equal(outs[0], ref[0]) and torch.equal(outs[1], ref[1])
 
 
+def test_most_rows():
+    """2^24 rows: more blocks than a grid's second dimension holds."""
+    M, K = 1 << 24, 16
+    g = torch.Generator(device=DEV).manual_seed(31)
+    x = torch.randn(M, K, generator=g, device=DEV).to(BF)
+    W = torch.randn(3, K, generator=g, device=DEV).to(BF)
+    got = moe.linear(x, W, out_dtype=F32)
+    rows = torch.cat([torch.arange(64), torch.arange(M // 2, M // 2 + 64),
+                      torch.arange(M - 64, M)]).to(DEV)
+    y, dy = reference(x[rows], [W.double()], [None], None, "none")
+    check(got[rows], y, dy)
+    far = (got - x.float() @ W.float().t()).abs().max()
+    assert float(far) < 1e-4
+
+
 def test_no_rows():
     W = torch.randn(64, 64, device=DEV).to(BF)
     got = moe.linear(torch.empty(0, 64, dtype=BF, device=DEV), W)
