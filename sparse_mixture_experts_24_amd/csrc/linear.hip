@@ -679,10 +679,6 @@ static hipError_t launch_linear_t(const LinearArgs& a, hipStream_t s) {
     const double tile = steps * std::max(loads, mma) + 4000.0 + m * (double)w / 4.0;
     return (double)ceil_div(ceil_div(a.M, m) * ceil_div(a.N * (int64_t)out, w), cus) * tile;
   };
-  // Stages of the smallest tiles: as many as gain (gated 64 x 4096 x 14336: 53 us with 3 and 2
-  // stages in 64 x 32 and 32 x 32 tiles, 39 with 4 and 3; 24 x 4096 x 4096 18 and 14.4; 8-bit
-  // 33 and 25, though 14.4 against 13.5 for 83 x 70 x 5488).  Plain 64 x 32 tiles lose with 6
-  // (64 x 7168 x 2048 9.5 -> 9.9 us: a longer start).
   // float MFMAs bound every tile alike, and the registers of 256 x 256 spill (4096 x 4096 x
   // 4096 in 940 us, 919 without it)
   constexpr bool LARGE = sizeof(WT) != 4;
@@ -701,6 +697,10 @@ static hipError_t launch_linear_t(const LinearArgs& a, hipStream_t s) {
   const double rows = (double)ceil_div(blocks * per, cus) * (run + 8000.0);
   const double* best = std::min_element(t, t + 6);
   if (blocks <= kMaxGridY && rows < *best) return launch_rows<WT, GATED>(a, s);
+  // Stages of the smallest tiles: as many as gain (gated 64 x 4096 x 14336: 53 us with 3 and 2
+  // stages in 64 x 32 and 32 x 32 tiles, 39 with 4 and 3; 24 x 4096 x 4096 18 and 14.4; 8-bit
+  // 33 and 25, though 14.4 against 13.5 for 83 x 70 x 5488).  Plain 64 x 32 tiles lose with 6
+  // (64 x 7168 x 2048 9.5 -> 9.9 us: a longer start).
   switch ((int)(best - t)) {
     case 0:
       if constexpr (LARGE) return run_tiles<WT, 4, 2, 2, 4, 1, 2, GATED>(a, s);
